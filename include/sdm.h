@@ -316,6 +316,168 @@ SDM_API int sdm_gdn_forward(const void* q, const void* k, const void* v, const f
                             const sdm_gdn_dims* dims, void* workspace, size_t ws_bytes,
                             void* stream);
 
+/*
+ * ---- Sequence operators beside the recurrences ------------------------------
+ * The short causal convolution that stands before such layers, the selective
+ * state space scan (the dense-state comparator next to GDN), and sparse
+ * attention over blocks that a cheap score selects (the growing-memory
+ * counterpart of sdm_select and the SDM read).  They take strided views: a
+ * tensor [B][H][T][d] is a pointer and the element strides of b, h and t, its last
+ * axis dense, so that slices of one token-major projection are passed as they
+ * are.  Strides are not negative; input axes may be broadcast (stride 0).
+ * Pointers are aligned to their element (state tables S and workspaces: 16
+ * bytes); the fast variants are taken when bases and strides are multiples of 16
+ * bytes.  `lengths` [B] int32, NULL for full length, gives the live steps of each
+ * row of a padded batch; values outside [0, T] are clamped to it.  Gradients of
+ * inputs have the inputs' type, those of parameters, gates and states are
+ * float32.  No call uses atomics on results: equal calls give equal bits.
+ * Stream, workspace, aliasing and error conventions as sdm_forward; workspaces
+ * hold nothing between calls.
+ */
+typedef struct sdm_strides { int64_t b, h, t; } sdm_strides;
+
+/* Short causal convolution, one filter of K taps (2..8) per channel. */
+typedef struct sdm_conv_dims {
+  int32_t B, H, T, d; /* d channels per head; H * d filters */
+  int32_t K;          /* taps */
+  int32_t silu;       /* 1: y = p sigmoid(p), 0: y = p */
+  int32_t in_dtype;   /* of x, w, bias, state and y */
+} sdm_conv_dims;
+
+/*
+ * p_t = bias + sum_{i<K} w_i x_{t-K+1+i}, y = silu(p) or p.  w [H][d][K], bias
+ * [H][d] or NULL.  state_inout [B][H][K-1][d] (NULL: zeros, nothing kept) is read
+ * as the K - 1 inputs before the call and overwritten with the last K - 1 inputs
+ * (of the live steps), so one token at a time is T = 1 with the state carried.
+ * Steps at or past lengths[b] are not read and their y is 0.
+ */
+SDM_API int sdm_conv_forward(const void* x, const void* w, const void* bias, void* state_inout,
+                             const int32_t* lengths, void* y, const sdm_conv_dims* dims,
+                             const sdm_strides* sx, const sdm_strides* sy, void* stream);
+
+/*
+ * Gradients: dx (x's type), dw [H][d][K], dbias [H][d] (NULL: not wanted) and
+ * dstate0 [B][H][K-1][d] (NULL: not wanted), float32.  state0: the state the
+ * forward started from (a copy; NULL for zeros).  dstate: the gradient of the
+ * state it left, float32, NULL for 0.  T >= 1, full length: mask dy for padded steps.
+ */
+SDM_API size_t sdm_conv_backward_workspace_bytes(const sdm_conv_dims* dims);
+SDM_API int sdm_conv_backward(const void* x, const void* w, const void* bias, const void* state0,
+                              const void* dy, const float* dstate, void* dx, float* dw,
+                              float* dbias, float* dstate0, const sdm_conv_dims* dims,
+                              const sdm_strides* sx, const sdm_strides* sdy,
+                              const sdm_strides* sdx, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/* Selective state space scan. */
+typedef struct sdm_ssm_dims {
+  int32_t B, H;     /* batch, heads */
+  int32_t G;        /* groups sharing Bm and Cm; head h reads group h / (H / G) */
+  int32_t T;
+  int32_t d_k;      /* state width (columns of S): 16, 32, 64 or 128 */
+  int32_t d_v;      /* value width (rows of S): 16, 32, 64 or 128 */
+  int32_t in_dtype; /* of x, Bm, Cm and y */
+} sdm_ssm_dims;
+
+/* Views of x [B][H][T][d_v], dt [B][H][T], Bm, Cm [B][G][T][d_k], y [B][H][T][d_v]. */
+typedef struct sdm_ssm_views { sdm_strides x, dt, B, C, y; } sdm_ssm_views;
+
+/*
+ * Per (b,h) head, S in R^{d_v x d_k} as sdm_gdn_forward lays it out:
+ *     a_t = exp(dt_t A_h);  S_t = a_t S_{t-1} + dt_t x_t Bm_t^T;  y_t = S_t Cm_t + D_h x_t.
+ * dt float32 (>= 0, after its softplus), A [H] float32 (<= 0), D [H] float32 or
+ * NULL.  S_inout [B][H][d_v][d_k] float32: S_0 in, the last live state out.
+ * Steps at or past lengths[b] change nothing and their y is 0.  A step with
+ * dt = 0 leaves S as it is.
+ */
+SDM_API size_t sdm_ssm_workspace_bytes(const sdm_ssm_dims* dims);
+SDM_API int sdm_ssm_forward(const void* x, const float* dt, const float* A, const void* Bm,
+                            const void* Cm, const float* D, float* S_inout,
+                            const int32_t* lengths, void* y, const sdm_ssm_dims* dims,
+                            const sdm_ssm_views* views, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/* The same for one token or a few (the steps run in order): one kernel, no workspace. */
+SDM_API int sdm_ssm_step(const void* x, const float* dt, const float* A, const void* Bm,
+                         const void* Cm, const float* D, float* S_inout, void* y,
+                         const sdm_ssm_dims* dims, const sdm_ssm_views* views, void* stream);
+
+/*
+ * Gradients of sdm_ssm_forward at full length.  S0: the state it started from
+ * (NULL: zeros).  dS_T: gradient of the state it left (NULL: 0).  views.y: strides
+ * of dy; grad_views.x, dt, B, C: strides of dx, ddt, dB, dC (grad_views.y is not
+ * used).  dx, dB, dC have the inputs' type; ddt, dA [H], dD [H] (NULL: not
+ * wanted) and dS0 [B][H][d_v][d_k] (NULL: not wanted) are float32.  dB and dC are
+ * summed over their group's heads.  T >= 1.  The workspace holds the states and
+ * their gradients at chunk starts and grows with T.
+ */
+SDM_API size_t sdm_ssm_backward_workspace_bytes(const sdm_ssm_dims* dims);
+SDM_API int sdm_ssm_backward(const void* x, const float* dt, const float* A, const void* Bm,
+                             const void* Cm, const float* D, const float* S0, const void* dy,
+                             const float* dS_T, void* dx, float* ddt, float* dA, void* dB,
+                             void* dC, float* dD, float* dS0, const sdm_ssm_dims* dims,
+                             const sdm_ssm_views* views, const sdm_ssm_views* grad_views,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Sparse attention over selected blocks. */
+typedef struct sdm_block_dims {
+  int32_t B, H;     /* batch, query heads */
+  int32_t G;        /* key heads (groups); head h reads group h / (H / G) */
+  int32_t Tq, Tk;   /* queries are the last Tq of each row's keys; Tq <= Tk */
+  int32_t d;        /* head width: 32, 64 or 128 */
+  int32_t block;    /* keys per block: 32, 64 or 128 */
+  int32_t n_sel;    /* list length per query, 1..64 */
+  int32_t in_dtype; /* of q, k, v, the means and o */
+  float scale;      /* of q.k in the softmax (finite) */
+} sdm_block_dims;
+
+/* Views of q [B][H][Tq][d], k, v [B][G][Tk][d], o [B][H][Tq][d] and of the block
+ * means kc [B][G][n_means][d] (its t stride is from block to block). */
+typedef struct sdm_block_views { sdm_strides q, k, v, o, kc; } sdm_block_views;
+
+/* Means of the complete blocks first .. Tk / block - 1 of k, into kc: summed in
+ * float64, rounded once to k's type. */
+SDM_API int sdm_block_pool(const void* k, void* kc, int32_t first, const sdm_block_dims* dims,
+                           const sdm_block_views* views, void* stream);
+
+/*
+ * Lists idx [B][G][Tq][n_sel] (dense int32).  The query at position p (query i of
+ * row b: lengths[b] - Tq + i) gets its own block p / block first, then the best
+ * n_sel - 1 of the blocks before it by sum over the group's heads of q_h . kc_j,
+ * best first, lower index at ties, then -1.  Blocks that score -inf or NaN are not
+ * listed; a query with p < 0 gets -1 throughout.  Scores are float64 sums.  n_means
+ * >= (Tk - 1) / block means have to be there.
+ */
+SDM_API int sdm_block_select(const void* q, const void* kc, int32_t n_means,
+                             const int32_t* lengths, int32_t* idx, const sdm_block_dims* dims,
+                             const sdm_block_views* views, void* stream);
+
+/*
+ * o = softmax over the keys at positions <= p of the listed blocks, any lists: an
+ * entry outside [0, blocks) or behind p adds nothing, a repeated one counts as
+ * often as it is listed.  lse [B][H][Tq] float32 (NULL: not wanted) gets the log of
+ * the softmax sum.  A query without keys has o = 0 and lse = -inf.  Keys that no
+ * live query may see are not read.
+ */
+SDM_API size_t sdm_block_workspace_bytes(const sdm_block_dims* dims);
+SDM_API int sdm_block_forward(const void* q, const void* k, const void* v, const int32_t* idx,
+                              const int32_t* lengths, void* o, float* lse,
+                              const sdm_block_dims* dims, const sdm_block_views* views,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of sdm_block_forward at its lists, in the inputs' type; o and lse as it
+ * wrote them.  grad_views.q, k, v: strides of dq, dk, dv; grad_views.o: of d_o.
+ * All Tk rows of dk and dv are written.  Tq >= 1.
+ */
+SDM_API size_t sdm_block_backward_workspace_bytes(const sdm_block_dims* dims);
+SDM_API int sdm_block_backward(const void* q, const void* k, const void* v, const int32_t* idx,
+                               const int32_t* lengths, const void* o, const float* lse,
+                               const void* d_o, void* dq, void* dk, void* dv,
+                               const sdm_block_dims* dims, const sdm_block_views* views,
+                               const sdm_block_views* grad_views, void* workspace,
+                               size_t ws_bytes, void* stream);
+
 /* Library version, major*10000 + minor*100 + patch. */
 SDM_API int sdm_version(void);
 

@@ -11,3 +11,7 @@ from .sdm import (  # noqa: F401
     recur, backward,
     device_status, make_dims, query_plan, PLAN_FIELDS, gdn_forward, gdn_workspace_bytes, GdnDims,
 )
+from .sequence import (  # noqa: F401
+    conv_forward, conv_backward, ssm_forward, ssm_step, ssm_backward, ssm_workspace_bytes,
+    block_pool, block_select, block_forward, block_backward,
+)
