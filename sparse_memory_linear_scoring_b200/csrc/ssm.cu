@@ -413,11 +413,16 @@ extern "C" int sdm_ssm_forward(const void* x, const float* dt, const float* A, c
   if (!aligned_to(workspace, 16)) return SDM_ERR_ALIGN;
   SsmArgs a = ssm_args(dims, views);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  ssm_segments(dims, kSsmQ, &a);
+  const bool mma = ssm_tensor_sizes(dims) && view_aligned(x, a.sx, 2, 16) &&
+                   view_aligned(Bm, a.sB, 2, 16) && view_aligned(Cm, a.sC, 2, 16) &&
+                   view_aligned(y, a.sy, 2, 16);
+  ssm_segments(dims, mma ? kSsmQT : kSsmQ, &a);
   float* segS = static_cast<float*>(workspace);
   float* segG = segS + size_t(a.B) * a.H * a.nseg * a.P * a.N;
   cudaError_t e;
-  if (dims->in_dtype == SDM_DTYPE_BF16)
+  if (mma)
+    e = launch_ssm_fwd_mma(a, x, dt, A, Bm, Cm, D, S_inout, lengths, y, segS, segG, s);
+  else if (dims->in_dtype == SDM_DTYPE_BF16)
     e = launch_ssm_fwd_simt<__nv_bfloat16>(a, x, dt, A, Bm, Cm, D, S_inout, lengths, y, segS, segG, s);
   else
     e = launch_ssm_fwd_simt<float>(a, x, dt, A, Bm, Cm, D, S_inout, lengths, y, segS, segG, s);

@@ -71,6 +71,16 @@ __device__ __forceinline__ float decay_between(float hi_t, float lo_t, float hi_
 cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, float* S_end, int BH,
                              int nseg, int PN, bool reverse, cudaStream_t s);
 
+// The tensor-core walk takes bf16 inputs of widths 64 and 128 whose views allow
+// 16-byte pieces.
+cudaError_t launch_ssm_fwd_mma(const SsmArgs& a, const void* x, const float* dt, const float* A,
+                               const void* Bm, const void* Cm, const float* D, float* S,
+                               const int32_t* lengths, void* y, float* segS, float* segG,
+                               cudaStream_t s);
+inline bool ssm_tensor_sizes(const sdm_ssm_dims* d) {
+  return d->in_dtype == SDM_DTYPE_BF16 && d->d_v >= 64 && d->d_k >= 64;
+}
+
 // Argument checks and sizes shared by the entry points.
 SsmArgs ssm_args(const sdm_ssm_dims* d, const sdm_ssm_views* v);
 int ssm_views_ok(const sdm_ssm_views* v);

@@ -1,0 +1,322 @@
+// ssm_mma.cu -- the selective scan's chunk walk on the tensor cores (bf16 inputs,
+// widths 64 and 128).  ssm_internal.cuh has the chunk formulas, ssm.cu the
+// segments.
+//
+// A CTA walks one segment of one head in chunks of 64 steps.  Warp w owns rows
+// 16 w .. 16 w + 15 of S, which stay in its registers as float32 accumulators from
+// chunk to chunk; the chunk's x, B and C tiles arrive by cp.async one chunk ahead.
+// Per chunk:
+//   scores G = C B^T, weights M = mask exp(g_t - g_j) dt_j G (bf16 for the next
+//   product: one rounding of a weight, below that of y itself),
+//   y = M x + exp(g_t) (C S^T) + D x   (S rounded to bf16 for this product only),
+//   S = exp(g_Q) S + (w x)^T B with w_j = exp(g_Q - g_j) dt_j.
+// S itself is an output in float32 and is carried over thousands of steps, so w x is
+// split into three bf16 parts (what is left is below 2^-24) against the exact B:
+// three times the products of that term, which a bf16 or even a two-part (2^-16)
+// operand would make 400 or 2 times less exact than float32 sums.
+#include "mma_dev.cuh"
+#include "ssm_internal.cuh"
+
+namespace sdm {
+
+constexpr int kTQ = kSsmQT;  // 64
+
+template <int P, int N, bool OUT>
+struct SsmTile {
+  static constexpr int W = P / 16;                 // warps
+  static constexpr int LX = P + 8, LN = N + 8;     // pitches: ldmatrix without bank conflicts
+  static constexpr int X = kTQ * LX, BC = kTQ * LN;
+  static constexpr int STAGE = X + (OUT ? 2 : 1) * BC;   // bf16 elements
+  static constexpr int SB = OUT ? P * LN : 0;            // S rounded to bf16
+  static constexpr int LY = 72;
+  static constexpr int YS = OUT ? W * 16 * LY : 0;       // y rows on their way out
+  static constexpr int DEC = 5 * kTQ;                    // hi, lo, dt, exp(g), w
+  static constexpr size_t smem = size_t(2) * (2 * STAGE + SB + YS) + size_t(4) * 2 * DEC;
+};
+
+// Warp 0: decays of one chunk from its steps 2 lane, 2 lane + 1.
+__device__ __forceinline__ void tile_decay(float* dec, float d0, float d1, float A) {
+  float *hi = dec, *lo = dec + kTQ, *dts = dec + 2 * kTQ, *eg = dec + 3 * kTQ, *w = dec + 4 * kTQ;
+  const int lane = threadIdx.x & 31;
+  dts[2 * lane] = d0;
+  dts[2 * lane + 1] = d1;
+  __syncwarp();
+  chunk_decay<2>(dts, A, hi, lo);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = 2 * lane + i;
+    eg[t] = exp2f(hi[t] + lo[t]);
+    w[t] = decay_between(hi[kTQ - 1], lo[kTQ - 1], hi[t], lo[t]) * dts[t];
+  }
+}
+
+template <int P, int N, bool OUT>
+__global__ void __launch_bounds__(P * 2)
+k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restrict__ dt,
+           const float* __restrict__ A, const __nv_bfloat16* __restrict__ Bm,
+           const __nv_bfloat16* __restrict__ Cm, const float* __restrict__ D, float* __restrict__ S,
+           const int32_t* __restrict__ lengths, __nv_bfloat16* __restrict__ y,
+           float* __restrict__ segS, float* __restrict__ segG) {
+  using L = SsmTile<P, N, OUT>;
+  extern __shared__ __align__(16) unsigned char raw[];
+  __nv_bfloat16* st = reinterpret_cast<__nv_bfloat16*>(raw);
+  __nv_bfloat16* Sb = st + 2 * L::STAGE;
+  __nv_bfloat16* ys = Sb + L::SB;
+  float* dec = reinterpret_cast<float*>(ys + L::YS);
+  constexpr int NT = P * 2;
+  const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+  const int seg = blockIdx.x % a.nseg, bh = blockIdx.x / a.nseg;
+  const int b = bh / a.H, h = bh - b * a.H, gr = h / a.hg;
+  const int T = seq_len(lengths, b, a.T);
+  const float Ah = A[h], Dh = OUT && D ? D[h] : 0.f;
+  const int c0 = seg * a.cps, c1 = min(c0 + a.cps, a.nch);
+  // the state contribution of the last segment has no reader
+  if (!OUT && seg == a.nseg - 1) return;
+
+  auto load = [&](int c) {
+    __nv_bfloat16* s = st + (c & 1) * L::STAGE;
+    const int t0 = c * kTQ;
+    const uint32_t sx = smem_u32(s), sb = sx + 2 * L::X, sc = sb + 2 * L::BC;
+    for (int i = tid; i < kTQ * (P / 8); i += NT) {
+      const int t = i / (P / 8), e = (i % (P / 8)) * 8;
+      const bool in = t0 + t < T;
+      cp_async16(sx + 2 * (t * L::LX + e), x + row_off(a.sx, b, h, in ? t0 + t : 0) + e, in);
+    }
+    for (int i = tid; i < kTQ * (N / 8); i += NT) {
+      const int t = i / (N / 8), e = (i % (N / 8)) * 8;
+      const bool in = t0 + t < T;
+      const int tt = in ? t0 + t : 0;
+      cp_async16(sb + 2 * (t * L::LN + e), Bm + row_off(a.sB, b, gr, tt) + e, in);
+      if (OUT) cp_async16(sc + 2 * (t * L::LN + e), Cm + row_off(a.sC, b, gr, tt) + e, in);
+    }
+  };
+  auto dt_at = [&](int c, int i) {
+    const int t = c * kTQ + 2 * lane + i;
+    return c < c1 && t < T ? dt[row_off(a.sdt, b, h, t)] : 0.f;
+  };
+
+  // S rows 16 wp + g, + 8; columns 8 n + 2 q, + 1
+  const int g = lane >> 2, q = lane & 3;
+  float s[N / 8][4];
+  const size_t PN = size_t(P) * N;
+  float* slot = a.nseg > 1 ? segS + size_t(blockIdx.x) * PN : S + size_t(bh) * PN;
+#pragma unroll
+  for (int n = 0; n < N / 8; ++n) {
+    const float* p0 = slot + (16 * wp + g) * N + 8 * n + 2 * q;
+    float2 u = make_float2(0.f, 0.f), v = u;
+    if (OUT) {
+      u = *reinterpret_cast<const float2*>(p0);
+      v = *reinterpret_cast<const float2*>(p0 + 8 * N);
+    }
+    s[n][0] = u.x; s[n][1] = u.y; s[n][2] = v.x; s[n][3] = v.y;
+  }
+  auto put_state = [&]() {
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n) {
+      __nv_bfloat16* p0 = Sb + (16 * wp + g) * L::LN + 8 * n + 2 * q;
+      *reinterpret_cast<uint32_t*>(p0) = pack_bf16(s[n][0], s[n][1]);
+      *reinterpret_cast<uint32_t*>(p0 + 8 * L::LN) = pack_bf16(s[n][2], s[n][3]);
+    }
+  };
+  if (OUT) put_state();
+  load(c0);
+  cp_async_commit();
+  if (c0 + 1 < c1) load(c0 + 1);
+  cp_async_commit();
+  if (wp == 0) tile_decay(dec + (c0 & 1) * L::DEC, dt_at(c0, 0), dt_at(c0, 1), Ah);
+  float tot = 0.f;
+
+  for (int c = c0; c < c1; ++c) {
+    cp_async_wait<1>();
+    __syncthreads();  // chunk c's tiles, decays and bf16 state are in place
+    const __nv_bfloat16* xs = st + (c & 1) * L::STAGE;
+    const uint32_t ax = smem_u32(xs), ab = ax + 2 * L::X, ac = ab + 2 * L::BC;
+    const float* dc = dec + (c & 1) * L::DEC;
+    const float *hi = dc, *lo = dc + kTQ, *dts = dc + 2 * kTQ, *eg = dc + 3 * kTQ, *wj = dc + 4 * kTQ;
+    float nd0 = 0.f, nd1 = 0.f;
+    if (wp == 0) {  // next chunk's steps, read ahead
+      nd0 = dt_at(c + 1, 0);
+      nd1 = dt_at(c + 1, 1);
+    }
+    const int t0 = c * kTQ, live = T - t0;
+    if (OUT) {
+      const int rt = wp & 3, p0 = (wp >> 2) * 64;  // rows 16 rt.., columns p0 .. p0 + 63
+      float acc[8][4];
+      if (live > 16 * rt) {
+        float sc[8][4];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = sc[n][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < N; k += 16) {
+          uint32_t af[4];
+          ldsm4(af, ac + 2 * frag_a(lane, 16 * rt, k, L::LN));
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            if (n <= rt) {
+              uint32_t bf[4];
+              ldsm4(bf, ab + 2 * frag_b(lane, 16 * n, k, L::LN));
+              mma_bf16(sc[2 * n], af, bf[0], bf[1]);
+              mma_bf16(sc[2 * n + 1], af, bf[2], bf[3]);
+            }
+            uint32_t sf[4];
+            ldsm4(sf, smem_u32(Sb) + 2 * frag_b(lane, p0 + 16 * n, k, L::LN));
+            mma_bf16(acc[2 * n], af, sf[0], sf[1]);
+            mma_bf16(acc[2 * n + 1], af, sf[2], sf[3]);
+          }
+        }
+        const int ta = 16 * rt + g, tb = ta + 8;
+        const float ea = eg[ta], eb = eg[tb], ha = hi[ta], hb = hi[tb], la = lo[ta], lb = lo[tb];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          acc[n][0] *= ea; acc[n][1] *= ea;
+          acc[n][2] *= eb; acc[n][3] *= eb;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k <= rt) {
+            uint32_t mf[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int j = 16 * k + 8 * u + 2 * q;
+              const float2 hj = *reinterpret_cast<const float2*>(hi + j);
+              const float2 lj = *reinterpret_cast<const float2*>(lo + j);
+              const float2 dj = *reinterpret_cast<const float2*>(dts + j);
+              float* v = sc[2 * k + u];
+              const float m0 = j <= ta ? decay_between(ha, la, hj.x, lj.x) * dj.x * v[0] : 0.f;
+              const float m1 = j + 1 <= ta ? decay_between(ha, la, hj.y, lj.y) * dj.y * v[1] : 0.f;
+              const float m2 = j <= tb ? decay_between(hb, lb, hj.x, lj.x) * dj.x * v[2] : 0.f;
+              const float m3 = j + 1 <= tb ? decay_between(hb, lb, hj.y, lj.y) * dj.y * v[3] : 0.f;
+              mf[2 * u] = pack_bf16(m0, m1);
+              mf[2 * u + 1] = pack_bf16(m2, m3);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              uint32_t xf[4];
+              ldsm4t(xf, ax + 2 * frag_bt(lane, p0 + 16 * n, 16 * k, L::LX));
+              mma_bf16(acc[2 * n], mf, xf[0], xf[1]);
+              mma_bf16(acc[2 * n + 1], mf, xf[2], xf[3]);
+            }
+          }
+        }
+        // + D x, rows at or past the end are 0; through shared memory to 16-byte stores
+        __nv_bfloat16* yw = ys + wp * 16 * L::LY;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int e = 8 * n + 2 * q;
+          const uint32_t xa = *reinterpret_cast<const uint32_t*>(xs + ta * L::LX + p0 + e);
+          const uint32_t xb = *reinterpret_cast<const uint32_t*>(xs + tb * L::LX + p0 + e);
+          *reinterpret_cast<uint32_t*>(yw + g * L::LY + e) =
+              ta < live ? pack_bf16(fmaf(Dh, bf16_lo(xa), acc[n][0]), fmaf(Dh, bf16_hi(xa), acc[n][1])) : 0u;
+          *reinterpret_cast<uint32_t*>(yw + (g + 8) * L::LY + e) =
+              tb < live ? pack_bf16(fmaf(Dh, bf16_lo(xb), acc[n][2]), fmaf(Dh, bf16_hi(xb), acc[n][3])) : 0u;
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 3) + 4 * i, t = t0 + 16 * rt + r;
+        if (t < a.T) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (live > 16 * rt) v = *reinterpret_cast<const uint4*>(ys + (wp * 16 + r) * L::LY + (lane & 7) * 8);
+          *reinterpret_cast<uint4*>(y + row_off(a.sy, b, h, t) + p0 + (lane & 7) * 8) = v;
+        }
+      }
+    }
+    const float gq = hi[kTQ - 1] + lo[kTQ - 1];
+    tot += gq;
+    if (live > 0) {
+      // (w x)^T as A fragments in three parts, all 64 steps
+      uint32_t xw[4][3][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t xf[4];
+        ldsm4t(xf, ax + 2 * frag_at(lane, 16 * wp, 16 * k, L::LX));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 w = *reinterpret_cast<const float2*>(wj + 16 * k + (i >> 1) * 8 + 2 * q);
+          uint32_t u[3];
+          split_bf16<3>(bf16_lo(xf[i]) * w.x, bf16_hi(xf[i]) * w.y, u);
+          xw[k][0][i] = u[0]; xw[k][1][i] = u[1]; xw[k][2][i] = u[2];
+        }
+      }
+      const float eq = exp2f(gq);
+#pragma unroll
+      for (int n = 0; n < N / 16; ++n) {
+        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t bf[4];
+          ldsm4t(bf, ab + 2 * frag_bt(lane, 16 * n, 16 * k, L::LN));
+#pragma unroll
+          for (int i = 2; i >= 0; --i) {  // small parts first
+            mma_bf16(d0, xw[k][i], bf[0], bf[1]);
+            mma_bf16(d1, xw[k][i], bf[2], bf[3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[2 * n][i] = fmaf(eq, s[2 * n][i], d0[i]);
+          s[2 * n + 1][i] = fmaf(eq, s[2 * n + 1][i], d1[i]);
+        }
+      }
+    }
+    if (wp == 0 && c + 1 < c1) tile_decay(dec + ((c + 1) & 1) * L::DEC, nd0, nd1, Ah);
+    __syncthreads();  // everyone is done with chunk c's tiles and state
+    if (OUT) put_state();
+    if (c + 2 < c1) load(c + 2);
+    cp_async_commit();
+  }
+  cp_async_wait<0>();
+  float* out = OUT ? S + size_t(bh) * PN : slot;
+  if (!OUT || seg == a.nseg - 1) {
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n) {
+      float* p0 = out + (16 * wp + g) * N + 8 * n + 2 * q;
+      *reinterpret_cast<float2*>(p0) = make_float2(s[n][0], s[n][1]);
+      *reinterpret_cast<float2*>(p0 + 8 * N) = make_float2(s[n][2], s[n][3]);
+    }
+  }
+  if (!OUT && tid == 0) segG[blockIdx.x] = tot;
+}
+
+template <int P, int N>
+static cudaError_t launch_tile(const SsmArgs& a, const void* x, const float* dt, const float* A,
+                               const void* Bm, const void* Cm, const float* D, float* S,
+                               const int32_t* lengths, void* y, float* segS, float* segG,
+                               cudaStream_t s) {
+  using bf = __nv_bfloat16;
+  const unsigned grid = unsigned(a.B * a.H) * unsigned(a.nseg);
+  cudaError_t e;
+  if (a.nseg > 1) {
+    const int sm = int(SsmTile<P, N, false>::smem);
+    if ((e = cudaFuncSetAttribute(k_ssm_tile<P, N, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)) != cudaSuccess)
+      return e;
+    k_ssm_tile<P, N, false><<<grid, P * 2, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm,
+                                                   D, S, lengths, (bf*)y, segS, segG);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_ssm_carry(segS, segG, S, nullptr, a.B * a.H, a.nseg, P * N, false, s)) != cudaSuccess)
+      return e;
+  }
+  const int sm = int(SsmTile<P, N, true>::smem);
+  if ((e = cudaFuncSetAttribute(k_ssm_tile<P, N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)) != cudaSuccess)
+    return e;
+  k_ssm_tile<P, N, true><<<grid, P * 2, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm, D,
+                                                S, lengths, (bf*)y, segS, segG);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ssm_fwd_mma(const SsmArgs& a, const void* x, const float* dt, const float* A,
+                               const void* Bm, const void* Cm, const float* D, float* S,
+                               const int32_t* lengths, void* y, float* segS, float* segG,
+                               cudaStream_t s) {
+  if (a.P == 64)
+    return a.N == 64 ? launch_tile<64, 64>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s)
+                     : launch_tile<64, 128>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s);
+  return a.N == 64 ? launch_tile<128, 64>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s)
+                   : launch_tile<128, 128>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s);
+}
+
+}  // namespace sdm

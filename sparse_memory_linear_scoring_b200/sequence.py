@@ -331,7 +331,7 @@ def ssm_backward(x, dt, A, Bm, Cm, S0, dy, dS_T=None, *, D=None,
                  workspace: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
     """Gradients of ssm_forward at full length (sdm_ssm_backward).  S0: the state it
     started from (a copy; None for zeros); dS_T: the gradient of the state it left
-    (None: 0).  Returns x, B, C (x's dtype), dt [B,H,T], A [H], S0 [B,H,d_v,d_k] and,
+    (None: 0).  Returns x, Bm, Cm (x's dtype), dt [B,H,T], A [H], S0 [B,H,d_v,d_k] and,
     where D is given, D [H], float32."""
     dims = _ssm_args(x, dt, A, Bm, Cm, D)
     B, H, P, N = dims.B, dims.H, dims.d_v, dims.d_k
@@ -347,15 +347,15 @@ def ssm_backward(x, dt, A, Bm, Cm, S0, dy, dS_T=None, *, D=None,
         _check(lib.sdm_ssm_backward(*([None] * 16), ctypes.byref(dims), None, None, None, 0, None))
     with _On(dev, stream) as s:
         f32 = dict(dtype=torch.float32, device=dev)
-        g = {"x": _like(x), "dt": _like(dt), "A": torch.empty(H, **f32), "B": _like(Bm),
-             "C": _like(Cm), "S0": torch.empty(B, H, P, N, **f32)}
+        g = {"x": _like(x), "dt": _like(dt), "A": torch.empty(H, **f32), "Bm": _like(Bm),
+             "Cm": _like(Cm), "S0": torch.empty(B, H, P, N, **f32)}
         if D is not None:
             g["D"] = torch.empty(H, **f32)
         ws = _workspace_for(need, workspace, dev)
-        v, gv = _ssm_views(x, dt, Bm, Cm, dy), _ssm_views(g["x"], g["dt"], g["B"], g["C"], g["x"])
+        v, gv = _ssm_views(x, dt, Bm, Cm, dy), _ssm_views(g["x"], g["dt"], g["Bm"], g["Cm"], g["x"])
         _check(lib.sdm_ssm_backward(
             _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(S0), _ptr(dy), _ptr(dS_T),
-            _ptr(g["x"]), _ptr(g["dt"]), _ptr(g["A"]), _ptr(g["B"]), _ptr(g["C"]), _ptr(g.get("D")),
+            _ptr(g["x"]), _ptr(g["dt"]), _ptr(g["A"]), _ptr(g["Bm"]), _ptr(g["Cm"]), _ptr(g.get("D")),
             _ptr(g["S0"]), ctypes.byref(dims), ctypes.byref(v), ctypes.byref(gv), _ptr(ws),
             _nbytes(ws), s))
     return g

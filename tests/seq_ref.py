@@ -97,7 +97,7 @@ def ssm_grads(x, dt, A, Bm, Cm, S0, dy, dST, D, magnitude=False):
     if D is not None:
         dx = dx + D.double()[None, :, None, None] * dy
     fold = lambda t: t.reshape(B, G, H // G, T, N).sum(2)  # noqa: E731
-    return dict(x=dx, dt=xu + A[None, :, None] * q, A=(dt * q).sum((0, 2)), B=fold(dB), C=fold(dC),
+    return dict(x=dx, dt=xu + A[None, :, None] * q, A=(dt * q).sum((0, 2)), Bm=fold(dB), Cm=fold(dC),
                 S0=R, D=(x * dy).sum((0, 2, 3)))
 
 

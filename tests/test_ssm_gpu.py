@@ -153,7 +153,7 @@ def test_backward(B, H, G, T, P, N, dtype, layout, decay):
     # what stays in float32: products of exact inputs, the states as bf16 parts that leave
     # less than 2^-17 of them
     k32 = (64 + 2 * max(P, N) + T / 32 + 16) * R.ADD + 2.0 ** -17
-    for n in ("x", "B", "C"):
+    for n in ("x", "Bm", "Cm"):
         assert out[n].dtype == dtype
         R.close(out[n], ref[n], k16 * mag[n], "d" + n)
     for n in ("dt", "S0"):
@@ -188,8 +188,8 @@ def test_backward_is_the_slope():
         y = sdm.ssm_forward(c["x"], c["dt"], c["A"], c["Bm"], c["Cm"], S, c["D"])
         return float((y.double() * dy.double()).sum() + (S.double() * dS.double()).sum())
 
-    for n, m, h in (("x", "x", 1e-2), ("dt", "dt", 1e-4), ("A", "A", 1e-2), ("Bm", "B", 1e-2),
-                    ("Cm", "C", 1e-2), ("S", "S0", 1e-2), ("D", "D", 1e-2)):
+    for n, m, h in (("x", "x", 1e-2), ("dt", "dt", 1e-4), ("A", "A", 1e-2), ("Bm", "Bm", 1e-2),
+                    ("Cm", "Cm", 1e-2), ("S", "S0", 1e-2), ("D", "D", 1e-2)):
         v = torch.randn(a[n].shape, generator=g, device="cuda")
         slope = (f({**a, n: a[n] + h * v}) - f({**a, n: a[n] - h * v})) / (2 * h)
         got = float((out[m].double() * v.double()).sum())
