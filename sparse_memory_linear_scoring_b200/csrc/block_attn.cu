@@ -196,7 +196,8 @@ cudaError_t launch_blk_row_bwd(const BlkArgs& a, bool bf16, const void* q, const
 using namespace sdm;
 
 extern "C" size_t sdm_block_workspace_bytes(const sdm_block_dims* dims) {
-  return blk_check(dims) == SDM_OK ? 16 : 0;
+  if (blk_check(dims) != SDM_OK) return 0;
+  return blk_tiles_pay(dims) ? blk_fwd_ws(dims, blk_chunk(dims), nullptr).bytes : 16;
 }
 
 extern "C" int sdm_block_forward(const void* q, const void* k, const void* v, const int32_t* idx,
@@ -215,7 +216,10 @@ extern "C" int sdm_block_forward(const void* q, const void* k, const void* v, co
   if (!workspace || ws_bytes < sdm_block_workspace_bytes(dims)) return SDM_ERR_WORKSPACE;
   if (!aligned_to(workspace, 16)) return SDM_ERR_ALIGN;
   const BlkArgs a = blk_args(dims, views, lengths);
-  const cudaError_t e = launch_blk_row_fwd(a, dims->in_dtype == SDM_DTYPE_BF16, q, k, v, idx, o, lse,
-                                           static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool tiles = blk_tiles_pay(dims) && view_aligned(q, a.sq, 2, 16) && view_aligned(k, a.sk, 2, 16) &&
+                     view_aligned(v, a.sv, 2, 16) && view_aligned(o, a.so, 2, 16);
+  const cudaError_t e = tiles ? launch_blk_fwd_mma(dims, a, q, k, v, idx, o, lse, workspace, s)
+                              : launch_blk_row_fwd(a, dims->in_dtype == SDM_DTYPE_BF16, q, k, v, idx, o, lse, s);
   return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }

@@ -146,7 +146,7 @@ static size_t blk_delta_bytes(const sdm_block_dims* d) {
 
 extern "C" size_t sdm_block_backward_workspace_bytes(const sdm_block_dims* dims) {
   if (blk_check(dims) != SDM_OK) return 0;
-  const size_t n = blk_delta_bytes(dims) + blk_plan(dims, nullptr).bytes;
+  const size_t n = blk_delta_bytes(dims) + blk_plan(dims, dims->Tq, 512, nullptr).bytes;
   return n > 0 ? n : 16;
 }
 
@@ -169,7 +169,7 @@ extern "C" int sdm_block_backward(const void* q, const void* k, const void* v, c
   if (!aligned_to(workspace, 16)) return SDM_ERR_ALIGN;
   const BlkArgs a = blk_args(dims, views, lengths);
   float* delta = static_cast<float*>(workspace);
-  const BlkPlan pl = blk_plan(dims, static_cast<char*>(workspace) + blk_delta_bytes(dims));
+  const BlkPlan pl = blk_plan(dims, dims->Tq, 512, static_cast<char*>(workspace) + blk_delta_bytes(dims));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = dims->in_dtype == SDM_DTYPE_BF16;
   cudaError_t e = launch_blk_row_bwd(a, bf, q, k, v, idx, o, lse, d_o, delta, dq, grad_views->o, grad_views->q, s);

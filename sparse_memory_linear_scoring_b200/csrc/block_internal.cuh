@@ -15,12 +15,14 @@ struct BlkArgs {
   int B, H, G, R;       // R = H / G heads per group
   int Tq, Tk, d, bs, n_sel;
   int nb;               // blocks, the last one possibly partial
+  int q0, nq;           // queries of this pass: [q0, q0 + nq) of Tq
   float scale;
   sdm_strides sq, sk, sv, so;
   const int32_t* lengths;
 };
 
-// Position of query 0 of batch b (negative: that many queries have no key).
+// Position of query 0 of batch b, counted from the call's first query (negative:
+// that many queries have no key).
 __device__ __forceinline__ int blk_pos0(const BlkArgs& a, int b) {
   return seq_len(a.lengths, b, a.Tk) - a.Tq;
 }
@@ -33,17 +35,47 @@ __device__ __forceinline__ int blk_keys(const BlkArgs& a, int j, int p) {
   return n < 0 ? 0 : (n > a.bs ? a.bs : n);
 }
 
-// The plan: for every (b, group), the (query, list slot) pairs of each block in
-// query order, as entry = query * n_sel + slot.
+// The plan of a pass over nq queries: for every (b, group), the (query, list slot)
+// pairs of each block in query order, as entry = (query - q0) * n_sel + slot, and the
+// blocks' rows (pair, head of the group) cut into items of at most `rows` rows.
 struct BlkPlan {
   int seg, nseg;         // queries per counting segment, segments
+  int rows;              // rows per item
+  int most;              // items per (b, group), at most
   int* hist;             // [BG][nseg][nb] counts, then first positions
   int* first;            // [BG][nb + 1] first entry of each block
-  int* entry;            // [BG][Tq * n_sel]
+  int* item;             // [BG][nb + 1] first item of each block
+  int* entry;            // [BG][nq * n_sel]
   size_t bytes;
 };
-BlkPlan blk_plan(const sdm_block_dims* d, void* base);
+BlkPlan blk_plan(const sdm_block_dims* d, int nq, int rows, void* base);
+
+// The block of an item (binary search in the items' first numbers), -1 behind the last.
+__device__ __forceinline__ int blk_of_item(const int* item, int nb, int it) {
+  if (it >= item[nb]) return -1;
+  int lo = 0, hi = nb - 1;  // item[lo] <= it < item[hi + 1]
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (item[mid] <= it) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
 cudaError_t launch_blk_plan(const BlkArgs& a, const BlkPlan& p, const int32_t* idx, cudaStream_t s);
+
+// Tensor-core forward pass (block_mma.cu): block by block over the lists' pairs,
+// partial results per (query, slot, head), then a join.
+struct BlkFwdWs {
+  BlkPlan plan;
+  float2* ml;      // [BG][nq][n_sel][R] log-sum-exp (base 2) and scale of each partial row
+  void* part;      // [BG][nq][n_sel][R][d] half
+  size_t bytes;
+};
+BlkFwdWs blk_fwd_ws(const sdm_block_dims* d, int nq, void* base);
+int blk_chunk(const sdm_block_dims* d);        // queries per pass
+bool blk_tiles_pay(const sdm_block_dims* d);   // whether the tensor-core pass is taken
+cudaError_t launch_blk_fwd_mma(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,
+                               const void* v, const int32_t* idx, void* o, float* lse,
+                               void* workspace, cudaStream_t s);
 
 int blk_check(const sdm_block_dims* d);
 BlkArgs blk_args(const sdm_block_dims* d, const sdm_block_views* v, const int32_t* lengths);

@@ -163,11 +163,11 @@ k_blk_count(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
   for (int j = threadIdx.x; j < a.nb; j += 256) cnt[j] = 0;
   __syncthreads();
   const int pos0 = blk_pos0(a, bg / a.G);
-  const int q0 = sg * p.seg, n = min(p.seg, a.Tq - q0) * a.n_sel;
-  const int32_t* ip = idx + ((size_t)bg * a.Tq + q0) * a.n_sel;
+  const int q0 = sg * p.seg, n = min(p.seg, a.nq - q0) * a.n_sel;
+  const int32_t* ip = idx + ((size_t)bg * a.Tq + a.q0 + q0) * a.n_sel;
   for (int i = threadIdx.x; i < n; i += 256) {
     const int j = ip[i];
-    if (blk_keys(a, j, pos0 + q0 + i / a.n_sel) > 0) atomicAdd(&cnt[j], 1);
+    if (blk_keys(a, j, pos0 + a.q0 + q0 + i / a.n_sel) > 0) atomicAdd(&cnt[j], 1);
   }
   __syncthreads();
   int* o = p.hist + (size_t)blockIdx.x * a.nb;
@@ -176,51 +176,56 @@ k_blk_count(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
 
 __global__ void __launch_bounds__(1024)
 k_blk_offsets(BlkArgs a, BlkPlan p) {
-  __shared__ int wsum[32];
-  __shared__ int carry;
+  __shared__ int2 wsum[32];
   const int bg = blockIdx.x, tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   int* hist = p.hist + (size_t)bg * p.nseg * a.nb;
   int* first = p.first + (size_t)bg * (a.nb + 1);
-  if (tid == 0) carry = 0;
+  int* item = p.item + (size_t)bg * (a.nb + 1);
+  // inclusive scan of (pairs, items) over the CTA; `total` gets the sums
+  auto scan = [&](int2 v, int2* total) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+      if (lane >= o) { v.x += x; v.y += y; }
+    }
+    __syncthreads();
+    if (lane == 31) wsum[wp] = v;
+    __syncthreads();
+    int2 before = make_int2(0, 0), all = before;
+    for (int w = 0; w < 32; ++w) {
+      if (w < wp) { before.x += wsum[w].x; before.y += wsum[w].y; }
+      all.x += wsum[w].x; all.y += wsum[w].y;
+    }
+    *total = all;
+    return make_int2(v.x + before.x, v.y + before.y);
+  };
+  int2 carry = make_int2(0, 0);
   for (int j0 = 0; j0 < a.nb; j0 += 1024) {
     const int j = j0 + tid;
     int tot = 0;
     if (j < a.nb)
 #pragma unroll 8
       for (int s = 0; s < p.nseg; ++s) tot += hist[(size_t)s * a.nb + j];
-    int inc = tot;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    __syncthreads();
-    if (lane == 31) wsum[wp] = inc;
-    __syncthreads();
-    if (wp == 0) {
-      int v = wsum[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      wsum[lane] = v;
-    }
-    __syncthreads();
-    int at = carry + inc - tot + (wp ? wsum[wp - 1] : 0);
+    const int its = int(((long long)tot * a.R + p.rows - 1) / p.rows);
+    int2 sum;
+    const int2 inc = scan(make_int2(tot, its), &sum);
     if (j < a.nb) {
+      int at = carry.x + inc.x - tot;
       first[j] = at;
+      item[j] = carry.y + inc.y - its;
       for (int s = 0; s < p.nseg; ++s) {
         const int n = hist[(size_t)s * a.nb + j];
         hist[(size_t)s * a.nb + j] = at;
         at += n;
       }
     }
-    __syncthreads();
-    if (tid == 0) carry += wsum[31];
-    __syncthreads();
+    carry.x += sum.x;
+    carry.y += sum.y;
   }
-  if (tid == 0) first[a.nb] = carry;
+  if (tid == 0) {
+    first[a.nb] = carry.x;
+    item[a.nb] = carry.y;
+  }
 }
 
 __global__ void __launch_bounds__(32)
@@ -231,15 +236,15 @@ k_blk_place(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
   for (int j = lane; j < a.nb; j += 32) at[j] = h[j];
   __syncwarp();
   const int pos0 = blk_pos0(a, bg / a.G);
-  const int q0 = sg * p.seg, n = min(p.seg, a.Tq - q0) * a.n_sel;
-  const int32_t* ip = idx + ((size_t)bg * a.Tq + q0) * a.n_sel;
-  int* out = p.entry + (size_t)bg * a.Tq * a.n_sel;
+  const int q0 = sg * p.seg, n = min(p.seg, a.nq - q0) * a.n_sel;
+  const int32_t* ip = idx + ((size_t)bg * a.Tq + a.q0 + q0) * a.n_sel;
+  int* out = p.entry + (size_t)bg * a.nq * a.n_sel;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + lane;
     int j = -1;
     if (i < n) {
       j = ip[i];
-      if (blk_keys(a, j, pos0 + q0 + i / a.n_sel) == 0) j = -1;
+      if (blk_keys(a, j, pos0 + a.q0 + q0 + i / a.n_sel) == 0) j = -1;
     }
     const unsigned same = __match_any_sync(0xffffffffu, j);
     const int rank = __popc(same & ((1u << lane) - 1));
@@ -254,7 +259,7 @@ k_blk_place(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
   }
 }
 
-BlkPlan blk_plan(const sdm_block_dims* d, void* base) {
+BlkPlan blk_plan(const sdm_block_dims* d, int nq, int rows, void* base) {
   BlkPlan p;
   memset(&p, 0, sizeof(p));
   const size_t BG = size_t(d->B) * d->G;
@@ -262,8 +267,10 @@ BlkPlan blk_plan(const sdm_block_dims* d, void* base) {
   // segments of 128 queries, longer ones past 256 segments (the counts are
   // nseg x nb per group)
   p.seg = 128;
-  while ((d->Tq + (long long)p.seg - 1) / p.seg > 256) p.seg <<= 1;
-  p.nseg = (d->Tq + p.seg - 1) / p.seg;
+  while ((nq + (long long)p.seg - 1) / p.seg > 256) p.seg <<= 1;
+  p.nseg = (nq + p.seg - 1) / p.seg;
+  p.rows = rows;
+  p.most = int((long long)nq * d->n_sel * (d->H / d->G) / rows) + nb;
   char* b = static_cast<char*>(base);
   size_t o = 0;
   auto take = [&](size_t n) {
@@ -271,9 +278,11 @@ BlkPlan blk_plan(const sdm_block_dims* d, void* base) {
     o = (o + n * 4 + 255) & ~size_t(255);
     return q;
   };
-  p.hist = take(BG * p.nseg * nb);
+  // room for the most segments that so many queries or fewer can have
+  p.hist = take(BG * (nq > 128 * 256 ? 256 : (nq + 127) / 128) * nb);
   p.first = take(BG * (nb + 1));
-  p.entry = take(BG * d->Tq * d->n_sel);
+  p.item = take(BG * (nb + 1));
+  p.entry = take(BG * nq * d->n_sel);
   p.bytes = o;
   return p;
 }
@@ -300,7 +309,7 @@ int blk_check(const sdm_block_dims* d) {
       !(d->scale == d->scale && d->scale - d->scale == 0.f))
     return SDM_ERR_DIMS;
   if ((long long)d->B * d->H > (1 << 20) || (long long)d->B * d->H * d->Tq >= (1LL << 31) ||
-      (long long)d->Tq * d->n_sel >= (1LL << 31))
+      (long long)d->Tq * d->n_sel * (d->H / d->G) >= (1LL << 31))
     return SDM_ERR_DIMS;
   if ((d->d != 32 && d->d != 64 && d->d != 128) ||
       (d->block != 32 && d->block != 64 && d->block != 128) || d->n_sel > kSelMost ||
@@ -322,6 +331,7 @@ BlkArgs blk_args(const sdm_block_dims* d, const sdm_block_views* v, const int32_
   a.B = d->B; a.H = d->H; a.G = d->G; a.R = d->H / d->G;
   a.Tq = d->Tq; a.Tk = d->Tk; a.d = d->d; a.bs = d->block; a.n_sel = d->n_sel;
   a.nb = (d->Tk + d->block - 1) / d->block;
+  a.q0 = 0; a.nq = d->Tq;
   a.scale = d->scale;
   a.sq = v->q; a.sk = v->k; a.sv = v->v; a.so = v->o;
   a.lengths = lengths;

@@ -162,6 +162,30 @@ def test_unseen_keys_may_hold_anything(dtype):
     assert (g_["k"][0, :, 64:128] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("block,Tq", [(64, 200), (32, 20), (128, 200)])
+def test_later_values_stay_out(dtype, block, Tq):
+    """Infinite and NaN keys and values behind a query, in a block that it lists, leave it
+    as it is; the queries that see them do get them."""
+    q, k, v, _ = _make(1, 4, 2, Tq, 200, 64, dtype)
+    idx = R.select(q, R.pool(k, block), 3, block, 200)
+    ref = R.block_attention(q, k, v, idx, block, 0.125)
+    first = 200 - Tq
+    v[:, 0, 185] = float("inf")
+    v[:, 0, 190, :5] = float("nan")
+    k[:, 1, 195] = float("nan")
+    o = sdm.block_forward(q, k, v, idx, block=block)
+    for h, end in ((0, 185), (1, 185), (2, 195), (3, 195)):
+        n = end - first
+        one = {x: ref[x][:, h:h + 1, :n] for x in ("o", "o_mag", "smag")}
+        R.close(o[:, h:h + 1, :n], one["o"], _k(dtype, 64, one) * one["o_mag"], "head %d" % h)
+    lists = (idx[0, 0] == 185 // block).any(-1)  # the queries of group 0 that list the keys' block
+    mid, end = o[:, :2, 185 - first:190 - first], o[0, :2, 190 - first:][:, lists[190 - first:]]
+    assert lists[185 - first:190 - first].all() and (mid == math.inf).all()
+    assert end[..., :5].isnan().all() and (end[..., 5:] == math.inf).all()
+    assert o[:, 2:, 195 - first:].isnan().all()
+
+
 def _check_backward(q, k, v, idx, block, dtype, g, lengths=None, scale=None):
     d = q.shape[3]
     sc = d ** -0.5 if scale is None else scale
