@@ -146,7 +146,11 @@ static size_t blk_delta_bytes(const sdm_block_dims* d) {
 
 extern "C" size_t sdm_block_backward_workspace_bytes(const sdm_block_dims* dims) {
   if (blk_check(dims) != SDM_OK) return 0;
-  const size_t n = blk_delta_bytes(dims) + blk_plan(dims, dims->Tq, 512, nullptr).bytes;
+  size_t n = blk_delta_bytes(dims) + blk_plan(dims, dims->Tq, 512, nullptr).bytes;
+  if (blk_tiles_pay(dims)) {  // views that are not aligned still take the other path
+    const size_t t = blk_bwd_ws(dims, blk_bwd_chunk(dims), nullptr).bytes;
+    if (t > n) n = t;
+  }
   return n > 0 ? n : 16;
 }
 
@@ -168,9 +172,15 @@ extern "C" int sdm_block_backward(const void* q, const void* k, const void* v, c
   if (!workspace || ws_bytes < sdm_block_backward_workspace_bytes(dims)) return SDM_ERR_WORKSPACE;
   if (!aligned_to(workspace, 16)) return SDM_ERR_ALIGN;
   const BlkArgs a = blk_args(dims, views, lengths);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const sdm_block_views* gv = grad_views;
+  if (blk_tiles_pay(dims) && view_aligned(q, a.sq, 2, 16) && view_aligned(k, a.sk, 2, 16) &&
+      view_aligned(v, a.sv, 2, 16) && view_aligned(o, a.so, 2, 16) && view_aligned(d_o, gv->o, 2, 16) &&
+      view_aligned(dq, gv->q, 2, 16) && view_aligned(dk, gv->k, 2, 16) && view_aligned(dv, gv->v, 2, 16))
+    return launch_blk_bwd_mma(dims, a, q, k, v, idx, o, lse, d_o, dq, dk, dv, gv, workspace, s) == cudaSuccess
+               ? SDM_OK : SDM_ERR_CUDA;
   float* delta = static_cast<float*>(workspace);
   const BlkPlan pl = blk_plan(dims, dims->Tq, 512, static_cast<char*>(workspace) + blk_delta_bytes(dims));
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = dims->in_dtype == SDM_DTYPE_BF16;
   cudaError_t e = launch_blk_row_bwd(a, bf, q, k, v, idx, o, lse, d_o, delta, dq, grad_views->o, grad_views->q, s);
   if (e == cudaSuccess) e = launch_blk_plan(a, pl, idx, s);

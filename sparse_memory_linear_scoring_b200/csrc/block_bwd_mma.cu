@@ -1,0 +1,474 @@
+// block_bwd_mma.cu -- gradients of block-selected attention on the tensor cores (bf16).
+//
+// As in block_mma.cu a CTA takes one block of keys (64 at most) and up to kItemRows of
+// the rows (pair, head of the group) that list it, so that K and V stay in shared
+// memory and dK and dV in registers while the rows stream past, 64 at a time:
+//     P = exp(scale Q K^T - lse),  dS = P (dO V^T - delta) scale,
+//     dV += P^T dO,  dK += dS^T Q,  dQ part = dS K.
+// P and dS are rounded to bf16 once for the second products (2^-9 of a term, as the
+// results themselves).  Each warp owns 16 rows for P, dS and dQ, and 16 keys (or 16 keys
+// and half the columns) for dK and dV, whose operands it takes transposed from shared
+// memory.  A row's dQ is a sum over its list: parts are halves scaled by their
+// largest element (2^-12 beside the result's 2^-9), joined in list order.  dK and dV of
+// one item are float32 parts, joined in item order: no atomics, equal calls give equal
+// bits.  Without the parts a row's dQ would need a second walk over its list, which
+// reads K and V once more per query and recomputes P and dS, about half of all products.
+#include <cuda_fp16.h>
+
+#include "block_internal.cuh"
+#include "mma_dev.cuh"
+
+namespace sdm {
+
+constexpr int kGradRows = 512;   // rows per item
+constexpr int kGradTile = 64;    // rows per tile, 16 a warp
+constexpr int kGradThreads = 128;
+
+template <int D, int KT>
+struct GradTile {
+  static constexpr int ST = D <= 64 ? 2 : 1;   // row tiles in flight; at 128 a second CTA an SM does more
+  static constexpr int LD = D + 8, LP = KT + 8;
+  static constexpr int KV = KT * LD, RW = kGradTile * LD, PS = kGradTile * LP;
+  static constexpr size_t smem = size_t(2) * (2 * KV + ST * 2 * RW + 2 * PS) + 16;
+};
+
+template <int D, int KT>
+__global__ void __launch_bounds__(kGradThreads)
+k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
+           const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
+           const float* __restrict__ lse, const __nv_bfloat16* __restrict__ d_o, sdm_strides sdo) {
+  using L = GradTile<D, KT>;
+  extern __shared__ __align__(16) unsigned char raw[];
+  __nv_bfloat16* Ks = reinterpret_cast<__nv_bfloat16*>(raw);
+  __nv_bfloat16* Vs = Ks + L::KV;
+  __nv_bfloat16* Rs = Vs + L::KV;                  // [ST][Q, dO][64][LD]
+  __nv_bfloat16* Ps = Rs + L::ST * 2 * L::RW;      // [64][LP]
+  __nv_bfloat16* Ds = Ps + L::PS;
+  uint32_t* odd = reinterpret_cast<uint32_t*>(Ds + L::PS);  // keys with inf or NaN in K
+  const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+  const int g = lane >> 2, qd = lane & 3;
+  const int per = a.bs / KT, sub = blockIdx.x % per;
+  const int ii = blockIdx.x / per;
+  const int bg = ii / w.plan.most, it = ii - bg * w.plan.most;
+  const int b = bg / a.G, grp = bg - b * a.G;
+  const int* item = w.plan.item + (size_t)bg * (a.nb + 1);
+  const int j = blk_of_item(item, a.nb, it);
+  if (j < 0) return;
+  const int* first = w.plan.first + (size_t)bg * (a.nb + 1);
+  const int e0 = first[j], rows = (first[j + 1] - e0) * a.R;
+  const int r0 = (it - item[j]) * kGradRows, r1 = min(r0 + kGradRows, rows);
+  const int* entry = w.plan.entry + (size_t)bg * a.nq * a.n_sel + e0;
+  const int pos0 = blk_pos0(a, b);
+  const int k0 = j * a.bs + sub * KT, len = pos0 + a.Tq;  // keys at or past len are not read
+
+  if (tid < 2) odd[tid] = 0;
+  for (int i = tid; i < KT * (D / 8); i += kGradThreads) {
+    const int kk = i / (D / 8), c = (i % (D / 8)) * 8;
+    const bool in = k0 + kk < len;
+    const int at = in ? k0 + kk : 0;
+    cp_async16(smem_u32(Ks + kk * L::LD + c), k + row_off(a.sk, b, grp, at) + c, in);
+    cp_async16(smem_u32(Vs + kk * L::LD + c), v + row_off(a.sv, b, grp, at) + c, in);
+  }
+  auto fetch = [&](int base, int st) {  // the warp's own 16 rows of Q and dO
+    __nv_bfloat16* dq_ = Rs + st * 2 * L::RW + wp * 16 * L::LD;
+    const int row = base + 16 * wp + (lane & 15);
+    const bool in = row < r1;
+    const int e = in ? entry[row / a.R] : 0;
+    const int h = grp * a.R + (in ? row % a.R : 0), t = a.q0 + e / a.n_sel;
+    const unsigned long long sq = reinterpret_cast<unsigned long long>(q + row_off(a.sq, b, h, t));
+    const unsigned long long so = reinterpret_cast<unsigned long long>(d_o + row_off(sdo, b, h, t));
+    for (int i = lane; i < 16 * (D / 8); i += 32) {
+      const int r = i / (D / 8), c = (i % (D / 8)) * 8;
+      const __nv_bfloat16* pq = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, sq, r));
+      const __nv_bfloat16* po = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, so, r));
+      const bool ok = __shfl_sync(0xffffffffu, int(in), r) != 0;
+      cp_async16(smem_u32(dq_ + r * L::LD + c), pq + c, ok);
+      cp_async16(smem_u32(dq_ + L::RW + r * L::LD + c), po + c, ok);
+    }
+  };
+  fetch(r0, 0);
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncthreads();
+  for (int i = tid; i < KT * (D / 8); i += kGradThreads) {
+    const int kk = i / (D / 8);
+    const uint4 u = *reinterpret_cast<const uint4*>(Ks + kk * L::LD + (i % (D / 8)) * 8);
+    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    bool bad = false;
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      bad |= (x[z] & 0x7f80u) == 0x7f80u || (x[z] & 0x7f800000u) == 0x7f800000u;
+    if (bad) atomicOr(&odd[kk >> 5], 1u << (kk & 31));
+  }
+  __syncthreads();
+  const bool anyodd = (odd[0] | odd[KT / 32 - 1]) != 0;
+  const float c2 = a.scale * kLog2e;
+  const uint32_t ak = smem_u32(Ks), av = smem_u32(Vs), ap = smem_u32(Ps), ad = smem_u32(Ds);
+  // dK, dV: keys 16 ks.., columns cp DP..
+  constexpr int NK = KT / 16, DP = D * NK / 4;
+  const int ks = wp % NK, cp = (wp / NK) * DP;
+  float gk[DP / 8][4], gv[DP / 8][4];
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gk[n][i] = gv[n][i] = 0.f;
+
+  for (int base = r0, st = 0; base < r1; base += kGradTile, st ^= L::ST - 1) {
+    if (L::ST == 2 && base + kGradTile < r1) fetch(base + kGradTile, st ^ 1);
+    cp_async_commit();
+    const int ra = base + 16 * wp + g, rb = ra + 8;
+    int na = 0, nb = 0;  // keys of this tile the two rows see
+    size_t oa = 0, ob = 0;
+    float la = INFINITY, lb = INFINITY, da = 0.f, db = 0.f;
+    auto row = [&](int r, int& n, size_t& o, float& l2, float& dl) {
+      if (r >= r1) return;
+      const int e = entry[r / a.R], t = a.q0 + e / a.n_sel;
+      n = max(0, min(KT, pos0 + t - k0 + 1));
+      o = (((size_t)bg * a.nq * a.n_sel + e) * a.R + r % a.R) * per + sub;
+      const size_t at = ((size_t)b * a.H + grp * a.R + r % a.R) * a.Tq + t;
+      const float x = lse[at];
+      l2 = x == -INFINITY ? INFINITY : x * kLog2e;
+      dl = w.delta[at];
+    };
+    row(ra, na, oa, la, da);
+    row(rb, nb, ob, lb, db);
+    if (L::ST == 2) cp_async_wait<1>(); else cp_async_wait<0>();
+    __syncwarp();
+    const __nv_bfloat16* Qs = Rs + st * 2 * L::RW;
+    const uint32_t aq = smem_u32(Qs), ao = aq + 2 * L::RW;
+    uint32_t df[KT / 16][4];  // dS as an A operand
+    {
+      float sc[KT / 8][4], dp[KT / 8][4];
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[n][i] = dp[n][i] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D; kk += 16) {
+        uint32_t af[4], of[4];
+        ldsm4(af, aq + 2 * frag_a(lane, 16 * wp, kk, L::LD));
+        ldsm4(of, ao + 2 * frag_a(lane, 16 * wp, kk, L::LD));
+#pragma unroll
+        for (int n = 0; n < KT / 16; ++n) {
+          uint32_t bf[4];
+          ldsm4(bf, ak + 2 * frag_b(lane, 16 * n, kk, L::LD));
+          mma_bf16(sc[2 * n], af, bf[0], bf[1]);
+          mma_bf16(sc[2 * n + 1], af, bf[2], bf[3]);
+          ldsm4(bf, av + 2 * frag_b(lane, 16 * n, kk, L::LD));
+          mma_bf16(dp[2 * n], of, bf[0], bf[1]);
+          mma_bf16(dp[2 * n + 1], of, bf[2], bf[3]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n) {
+        float p[4], s[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int col = 8 * n + 2 * qd + i;
+          p[i] = col < na ? exp2f(fmaf(sc[n][i], c2, -la)) : 0.f;
+          p[2 + i] = col < nb ? exp2f(fmaf(sc[n][2 + i], c2, -lb)) : 0.f;
+          s[i] = col < na ? p[i] * (dp[n][i] - da) * a.scale : 0.f;
+          s[2 + i] = col < nb ? p[2 + i] * (dp[n][2 + i] - db) * a.scale : 0.f;
+        }
+        const int at = (16 * wp + g) * L::LP + 8 * n + 2 * qd;
+        const uint32_t s0 = pack_bf16(s[0], s[1]), s1 = pack_bf16(s[2], s[3]);
+        df[n >> 1][(n & 1) * 2] = s0;
+        df[n >> 1][(n & 1) * 2 + 1] = s1;
+        *reinterpret_cast<uint32_t*>(Ps + at) = pack_bf16(p[0], p[1]);
+        *reinterpret_cast<uint32_t*>(Ps + at + 8 * L::LP) = pack_bf16(p[2], p[3]);
+        *reinterpret_cast<uint32_t*>(Ds + at) = s0;
+        *reinterpret_cast<uint32_t*>(Ds + at + 8 * L::LP) = s1;
+      }
+    }
+    __syncthreads();  // all rows' Q, dO, P and dS are in place
+#pragma unroll
+    for (int kk = 0; kk < kGradTile; kk += 16) {
+      uint32_t pf[4], sf[4];
+      ldsm4t(pf, ap + 2 * frag_at(lane, 16 * ks, kk, L::LP));
+      ldsm4t(sf, ad + 2 * frag_at(lane, 16 * ks, kk, L::LP));
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n) {
+        uint32_t bf[4];
+        ldsm4t(bf, ao + 2 * frag_bt(lane, cp + 16 * n, kk, L::LD));
+        mma_bf16(gv[2 * n], pf, bf[0], bf[1]);
+        mma_bf16(gv[2 * n + 1], pf, bf[2], bf[3]);
+        ldsm4t(bf, aq + 2 * frag_bt(lane, cp + 16 * n, kk, L::LD));
+        mma_bf16(gk[2 * n], sf, bf[0], bf[1]);
+        mma_bf16(gk[2 * n + 1], sf, bf[2], bf[3]);
+      }
+    }
+    float acc[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    if (!anyodd) {
+#pragma unroll
+      for (int kk = 0; kk < KT / 16; ++kk)
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t bf[4];
+          ldsm4t(bf, ak + 2 * frag_bt(lane, 16 * n, 16 * kk, L::LD));
+          mma_bf16(acc[2 * n], df[kk], bf[0], bf[1]);
+          mma_bf16(acc[2 * n + 1], df[kk], bf[2], bf[3]);
+        }
+    } else {
+      // 0 times an infinite or NaN key is not 0: keys that a row does not see are left out by hand
+#pragma unroll
+      for (int kk = 0; kk < KT / 16; ++kk)
+        for (int y = 0; y < 16; ++y) {
+          const int src = (lane & ~3) | ((y >> 1) & 3);
+          const uint32_t wa = __shfl_sync(0xffffffffu, y < 8 ? df[kk][0] : df[kk][2], src);
+          const uint32_t wb = __shfl_sync(0xffffffffu, y < 8 ? df[kk][1] : df[kk][3], src);
+          const float xa = (y & 1) ? bf16_hi(wa) : bf16_lo(wa), xb = (y & 1) ? bf16_hi(wb) : bf16_lo(wb);
+          const int key = 16 * kk + y;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(Ks + key * L::LD + 8 * n + 2 * qd);
+            if (key < na) {
+              acc[n][0] = fmaf(xa, bf16_lo(u), acc[n][0]);
+              acc[n][1] = fmaf(xa, bf16_hi(u), acc[n][1]);
+            }
+            if (key < nb) {
+              acc[n][2] = fmaf(xb, bf16_lo(u), acc[n][2]);
+              acc[n][3] = fmaf(xb, bf16_hi(u), acc[n][3]);
+            }
+          }
+        }
+    }
+    float xa = 0.f, xb = 0.f;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float u = fabsf(acc[n][i]), z = fabsf(acc[n][2 + i]);
+        if (u < INFINITY) xa = fmaxf(xa, u);
+        if (z < INFINITY) xb = fmaxf(xb, z);
+      }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, o));
+      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, o));
+    }
+    xa = fmaxf(xa, 2.3509887e-38f);  // 2^-125: its reciprocal is still finite
+    xb = fmaxf(xb, 2.3509887e-38f);
+    const float va = 1.f / xa, vb = 1.f / xb;
+    if (qd == 0) {
+      if (ra < r1) w.mul[oa] = xa;
+      if (rb < r1) w.mul[ob] = xb;
+    }
+    __syncthreads();  // everyone has read this tile's rows, P and dS
+    __half* stage = reinterpret_cast<__half*>(Rs + st * 2 * L::RW + wp * 16 * L::LD);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      *reinterpret_cast<__half2*>(stage + g * L::LD + 8 * n + 2 * qd) =
+          __floats2half2_rn(acc[n][0] * va, acc[n][1] * va);
+      *reinterpret_cast<__half2*>(stage + (g + 8) * L::LD + 8 * n + 2 * qd) =
+          __floats2half2_rn(acc[n][2] * vb, acc[n][3] * vb);
+    }
+    __syncwarp();
+    __half* part = static_cast<__half*>(w.part);
+    for (int i = lane; i < 16 * (D / 8); i += 32) {
+      const int r = i / (D / 8), c = (i % (D / 8)) * 8;
+      const size_t ua = __shfl_sync(0xffffffffu, oa, (r & 7) * 4), ub = __shfl_sync(0xffffffffu, ob, (r & 7) * 4);
+      if (base + 16 * wp + r < r1)
+        *reinterpret_cast<uint4*>(part + (r < 8 ? ua : ub) * D + c) =
+            *reinterpret_cast<const uint4*>(stage + r * L::LD + c);
+    }
+    __syncwarp();  // before the next fetch into these rows
+    if (L::ST == 1 && base + kGradTile < r1) fetch(base + kGradTile, 0);
+  }
+  cp_async_wait<0>();
+  float* kp = w.kv + (size_t)blockIdx.x * 2 * KT * D;
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n) {
+    float* o = kp + (16 * ks + g) * D + cp + 8 * n + 2 * qd;
+    *reinterpret_cast<float2*>(o) = make_float2(gk[n][0], gk[n][1]);
+    *reinterpret_cast<float2*>(o + 8 * D) = make_float2(gk[n][2], gk[n][3]);
+    *reinterpret_cast<float2*>(o + KT * D) = make_float2(gv[n][0], gv[n][1]);
+    *reinterpret_cast<float2*>(o + (KT + 8) * D) = make_float2(gv[n][2], gv[n][3]);
+  }
+}
+
+// delta = do.o, D / 8 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(256)
+k_blk_delta(BlkArgs a, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ d_o,
+            sdm_strides sdo, float* __restrict__ delta) {
+  constexpr int LN = D / 8;
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
+  const int c = (threadIdx.x % LN) * 8;
+  const bool in = i < (long long)a.B * a.H * a.Tq;
+  float s = 0.f;
+  if (in) {
+    const int t = int(i % a.Tq), bh = int(i / a.Tq), b = bh / a.H, h = bh - b * a.H;
+    float x[8], y[8];
+    Vec<__nv_bfloat16, 8>::load(o + row_off(a.so, b, h, t) + c, x);
+    Vec<__nv_bfloat16, 8>::load(d_o + row_off(sdo, b, h, t) + c, y);
+#pragma unroll
+    for (int z = 0; z < 8; ++z) s = fmaf(x[z], y[z], s);
+  }
+#pragma unroll
+  for (int w = LN / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+  if (in && c == 0) delta[i] = s;
+}
+
+// A row of dq from its parts, in list order; pairs without keys have none.
+template <int D>
+__global__ void __launch_bounds__(256)
+k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ dq,
+         sdm_strides sdq, int kt) {
+  constexpr int LN = D / 8;
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
+  const int c = (threadIdx.x % LN) * 8;
+  if (i >= (long long)a.B * a.G * a.nq * a.R) return;
+  const int r = int(i % a.R), per = a.bs / kt;
+  const long long bt = i / a.R;
+  const int t = int(bt % a.nq), bg = int(bt / a.nq), b = bg / a.G, h = (bg - b * a.G) * a.R + r;
+  const int32_t* list = idx + ((size_t)bg * a.Tq + a.q0 + t) * a.n_sel;
+  const int p = blk_pos0(a, b) + a.q0 + t;
+  const __half* part = static_cast<const __half*>(w.part) + c;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < a.n_sel; ++s) {
+    const int n = blk_keys(a, list[s], p);
+    for (int u = 0; u * kt < n; ++u) {
+      const size_t at = (((size_t)bt * a.n_sel + s) * a.R + r) * per + u;
+      const float f = w.mul[at];
+      const uint4 x = *reinterpret_cast<const uint4*>(part + at * D);
+      const __half2* hx = reinterpret_cast<const __half2*>(&x);
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const float2 y = __half22float2(hx[z]);
+        acc[2 * z] = fmaf(f, y.x, acc[2 * z]);
+        acc[2 * z + 1] = fmaf(f, y.y, acc[2 * z + 1]);
+      }
+    }
+  }
+  Vec<__nv_bfloat16, 8>::store(dq + row_off(sdq, b, h, a.q0 + t) + c, acc);
+}
+
+// dk, dv of 4 columns of a key: the items of its block in order.  With several passes
+// over the queries, sum [2][BG][nb * block][D] carries the total from pass to pass.
+template <int D>
+__global__ void __launch_bounds__(256)
+k_blk_dkv(BlkArgs a, BlkBwdWs w, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
+          sdm_strides sdk, sdm_strides sdv, int kt, int begin, int end) {
+  constexpr int LN = D / 4;
+  long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int c = int(i % LN) * 4;
+  i /= LN;
+  if (i >= (long long)a.B * a.G * a.Tk) return;
+  const int key = int(i % a.Tk), bg = int(i / a.Tk), which = blockIdx.y;
+  const int j = key / a.bs, in = key - j * a.bs, sub = in / kt, per = a.bs / kt;
+  const int* item = w.plan.item + (size_t)bg * (a.nb + 1);
+  const int i0 = item[j], i1 = item[j + 1];
+  float* sum = w.sum + (((size_t)which * a.B * a.G + bg) * a.Tk + key) * D + c;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!begin) s = *reinterpret_cast<const float4*>(sum);
+  const float* p = w.kv + ((((size_t)bg * w.plan.most + i0) * per + sub) * 2 + which) * kt * D +
+                   (size_t)(in - sub * kt) * D + c;
+  const size_t step = (size_t)per * 2 * kt * D;
+#pragma unroll 4
+  for (int u = i0; u < i1; ++u, p += step) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  if (!end) {
+    *reinterpret_cast<float4*>(sum) = s;
+  } else {
+    const float f[4] = {s.x, s.y, s.z, s.w};
+    const int b = bg / a.G, g = bg - b * a.G;
+    __nv_bfloat16* o = which ? dv + row_off(sdv, b, g, key) : dk + row_off(sdk, b, g, key);
+    Vec<__nv_bfloat16, 4>::store(o + c, f);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+static int grad_keys(const sdm_block_dims* d) { return d->block < 64 ? 32 : 64; }
+
+// Queries per pass: as many as keep the parts of dq within 2 GiB (at least 128).
+int blk_bwd_chunk(const sdm_block_dims* d) {
+  const long long per = (long long)d->B * d->H * d->n_sel * (d->block / grad_keys(d)) * (d->d * 2 + 4);
+  long long n = (2LL << 30) / per;
+  if (n < 128) n = 128;
+  if (n > d->Tq) n = d->Tq;
+  if (n < 1) n = 1;
+  const long long passes = (d->Tq + n - 1) / n;  // even passes
+  return passes > 0 ? int((d->Tq + passes - 1) / passes) : 1;
+}
+
+BlkBwdWs blk_bwd_ws(const sdm_block_dims* d, int nq, void* base) {
+  BlkBwdWs w;
+  memset(&w, 0, sizeof(w));
+  const size_t BG = size_t(d->B) * d->G, per = size_t(d->block / grad_keys(d));
+  const size_t rows = size_t(d->B) * d->H * nq * d->n_sel * per;
+  char* b = static_cast<char*>(base);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    char* p = b + o;
+    o = (o + bytes + 255) & ~size_t(255);
+    return p;
+  };
+  // what does not depend on the pass comes first
+  w.delta = reinterpret_cast<float*>(take(size_t(d->B) * d->H * d->Tq * 4));
+  w.sum = reinterpret_cast<float*>(take(blk_bwd_chunk(d) < d->Tq ? 2 * BG * d->Tk * d->d * 4 : 0));
+  w.plan = blk_plan(d, nq, kGradRows, b + o);
+  take(w.plan.bytes);
+  w.mul = reinterpret_cast<float*>(take(rows * 4));
+  w.part = take(rows * d->d * 2);
+  w.kv = reinterpret_cast<float*>(take(BG * w.plan.most * d->block * 2 * d->d * 4));
+  w.bytes = o;
+  return w;
+}
+
+template <int D>
+static cudaError_t launch_grad(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,
+                               const void* v, const int32_t* idx, const void* o, const float* lse,
+                               const void* d_o, void* dq, void* dk, void* dv,
+                               const sdm_block_views* gv, void* workspace, cudaStream_t s) {
+  using bf = __nv_bfloat16;
+  const int chunk = blk_bwd_chunk(d), kt = grad_keys(d);
+  cudaError_t e;
+  for (int q0 = 0; q0 < d->Tq; q0 += chunk) {
+    a.q0 = q0;
+    a.nq = d->Tq - q0 < chunk ? d->Tq - q0 : chunk;
+    const BlkBwdWs w = blk_bwd_ws(d, a.nq, workspace);
+    if (q0 == 0) {
+      const long long n = (long long)a.B * a.H * a.Tq * (D / 8);
+      k_blk_delta<D><<<unsigned((n + 255) / 256), 256, 0, s>>>(a, (const bf*)o, (const bf*)d_o, gv->o, w.delta);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if ((e = launch_blk_plan(a, w.plan, idx, s)) != cudaSuccess) return e;
+    const long long grid = (long long)a.B * a.G * w.plan.most * (a.bs / kt);
+    if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+    auto go = [&](auto key) -> cudaError_t {
+      constexpr int KT = decltype(key)::value;
+      const int sm = int(GradTile<D, KT>::smem);
+      cudaError_t r = cudaFuncSetAttribute(k_blk_grad<D, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+      if (r != cudaSuccess) return r;
+      k_blk_grad<D, KT><<<unsigned(grid), kGradThreads, sm, s>>>(a, w, (const bf*)q, (const bf*)k,
+                                                                 (const bf*)v, lse, (const bf*)d_o, gv->o);
+      return cudaGetLastError();
+    };
+    e = kt == 32 ? go(std::integral_constant<int, 32>()) : go(std::integral_constant<int, 64>());
+    if (e != cudaSuccess) return e;
+    const long long nr = (long long)a.B * a.H * a.nq * (D / 8);
+    k_blk_dq<D><<<unsigned((nr + 255) / 256), 256, 0, s>>>(a, w, idx, (bf*)dq, gv->q, kt);
+    const long long nk = (long long)a.B * a.G * a.Tk * (D / 4);
+    k_blk_dkv<D><<<dim3(unsigned((nk + 255) / 256), 2), 256, 0, s>>>(
+        a, w, (bf*)dk, (bf*)dv, gv->k, gv->v, kt, q0 == 0, q0 + a.nq == d->Tq);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_blk_bwd_mma(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,
+                               const void* v, const int32_t* idx, const void* o, const float* lse,
+                               const void* d_o, void* dq, void* dk, void* dv,
+                               const sdm_block_views* gv, void* workspace, cudaStream_t s) {
+  if (a.d == 32) return launch_grad<32>(d, a, q, k, v, idx, o, lse, d_o, dq, dk, dv, gv, workspace, s);
+  if (a.d == 64) return launch_grad<64>(d, a, q, k, v, idx, o, lse, d_o, dq, dk, dv, gv, workspace, s);
+  return launch_grad<128>(d, a, q, k, v, idx, o, lse, d_o, dq, dk, dv, gv, workspace, s);
+}
+
+}  // namespace sdm

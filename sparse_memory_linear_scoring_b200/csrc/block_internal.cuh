@@ -1,5 +1,5 @@
 // block_internal.cuh -- sparse attention over selected blocks (block_select.cu,
-// block_attn.cu, block_bwd.cu, block_mma.cu): sizes, the plan, shared device code.
+// block_attn.cu, block_bwd.cu, block_mma.cu, block_bwd_mma.cu): sizes, the plan, shared device code.
 //
 // Keys are cut into blocks of `block` consecutive positions.  The query at
 // position p (the last Tq of the sequence's keys) has a list of blocks; it
@@ -76,6 +76,23 @@ bool blk_tiles_pay(const sdm_block_dims* d);   // whether the tensor-core pass i
 cudaError_t launch_blk_fwd_mma(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,
                                const void* v, const int32_t* idx, void* o, float* lse,
                                void* workspace, cudaStream_t s);
+
+// Tensor-core backward pass (block_bwd_mma.cu).
+struct BlkBwdWs {
+  float* delta;    // [B][H][Tq] do.o
+  float* sum;      // [2][BG][Tk][d] dk, dv so far, where there is more than one pass
+  BlkPlan plan;
+  float* mul;      // [BG][nq][n_sel][R][block / keys] scale of each part of dq
+  void* part;      // [BG][nq][n_sel][R][block / keys][d] half
+  float* kv;       // [BG][items][block / keys][2][keys][d] parts of dk, dv
+  size_t bytes;
+};
+BlkBwdWs blk_bwd_ws(const sdm_block_dims* d, int nq, void* base);
+int blk_bwd_chunk(const sdm_block_dims* d);
+cudaError_t launch_blk_bwd_mma(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,
+                               const void* v, const int32_t* idx, const void* o, const float* lse,
+                               const void* d_o, void* dq, void* dk, void* dv,
+                               const sdm_block_views* gv, void* workspace, cudaStream_t s);
 
 int blk_check(const sdm_block_dims* d);
 BlkArgs blk_args(const sdm_block_dims* d, const sdm_block_views* v, const int32_t* lengths);

@@ -230,8 +230,8 @@ k_blk_tile(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q,
       xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, o));
       xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, o));
     }
-    if (xa == 0.f) xa = 1.f;
-    if (xb == 0.f) xb = 1.f;
+    xa = fmaxf(xa, 2.3509887e-38f);  // 2^-125: its reciprocal is still finite
+    xb = fmaxf(xb, 2.3509887e-38f);
     const float va = 1.f / xa, vb = 1.f / xb;
     __half* stage = reinterpret_cast<__half*>(mine);
     __syncwarp();  // the warp has read its queries

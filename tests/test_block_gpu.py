@@ -212,6 +212,40 @@ def test_backward(B, H, G, Tq, Tk, d, block, n_sel, dtype, layout):
     _check_backward(q, k, v, idx, block, dtype, g)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("block,Tq", [(64, 200), (32, 20), (128, 200)])
+def test_backward_later_keys_stay_out(dtype, block, Tq):
+    """Infinite and NaN keys and values behind a query leave its gradient as it is."""
+    q, k, v, g = _make(1, 4, 2, Tq, 200, 64, dtype)
+    idx = R.select(q, R.pool(k, block), 3, block, 200)
+    d_o = torch.randn(q.shape, generator=g, device="cuda").to(dtype)
+    o, lse = sdm.block_forward(q, k, v, idx, block=block, return_lse=True)
+    good = sdm.block_backward(q, k, v, idx, o, lse, d_o, block=block)
+    k[:, 0, 195, :5], k[:, 1, 193], v[:, :, 196] = float("inf"), float("nan"), float("nan")
+    o, lse = sdm.block_forward(q, k, v, idx, block=block, return_lse=True)
+    got = sdm.block_backward(q, k, v, idx, o, lse, d_o, block=block)
+    assert torch.equal(got["q"][:, :, :Tq - 7], good["q"][:, :, :Tq - 7])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_small_values(dtype):
+    """Values and their gradients near the bottom of the type's range."""
+    q, k, v, g = _make(1, 4, 2, 150, 150, 64, dtype)
+    idx = R.select(q, R.pool(k, 64), 3, 64, 150)
+    v = (v.float() * 2.0 ** -124).to(dtype)
+    o = sdm.block_forward(q, k, v, idx)
+    ref = R.block_attention(q, k, v, idx, 64, 0.125)
+    R.close(o, ref["o"], _k(dtype, 64, ref) * ref["o_mag"], "o")
+
+
+def test_many_passes():
+    """Lists so long that queries are taken in passes, with repeated entries."""
+    q, k, v, g = _make(8, 64, 4, 300, 300, 128, BF)
+    idx = torch.randint(-1, 4, (8, 4, 300, 64), generator=g, device="cuda", dtype=torch.int32)
+    _check_forward(q, k, v, idx, 128, BF)
+    _check_backward(q, k, v, idx, 128, BF, g)
+
+
 def test_backward_is_the_slope():
     q, k, v, g = _make(1, 4, 2, 90, 90, 32, F32)
     idx = R.select(q, R.pool(k, 32), 2, 32, 90)
