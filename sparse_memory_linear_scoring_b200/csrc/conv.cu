@@ -4,19 +4,48 @@
 //   p_t = bias + sum_{i<K} w_i x_{t-K+1+i},   y = p  or  p sigmoid(p),
 //   dp = dy silu'(p),  dx_t = sum_i w_i dp_{t+K-1-i},  dw_i = sum_t dp_t x_{t-K+1+i}.
 //
-// Both directions move bytes and little else (2K + 5 flops an element against 4
-// bytes in bf16), so a thread keeps a window of the last K - 1 inputs of its 16
-// (forward) or 8 bytes (backward; the filter, its gradient and two windows share
-// the registers) of channels and walks a tile of steps: every input is read once
-// from DRAM, plus K - 1 rows a tile that its neighbour has brought into L2.
+// Both directions move bytes and little else, but not by much: 2K + 5 flops and two
+// special functions an element against 4 bytes in bf16, so a plain division (about 10
+// instructions) for the sigmoid would bound them.  A thread keeps the window of the
+// last K - 1 inputs of a few neighbouring channels -- 4 forward, 2 backward, where the
+// filter, its gradient and two windows share the registers -- and walks a tile of
+// steps with 8 rows of loads in flight; narrow threads leave room for enough warps to
+// cover the loads.  Every input is read once from DRAM, plus K - 1 rows a tile that
+// its neighbour has brought into L2.
 #include "seq_internal.cuh"
 
 namespace sdm {
 
 struct ConvArgs {
-  int B, H, T, d, tt, ntile;
+  int B, H, T, d, tt, ntile, wvec;
   sdm_strides sx, sy;
 };
+
+// 1 / (1 + exp(-p)) with the reciprocal unit (2^-23 relative); its results below 2^-126
+// are flushed, and far below 0 the sigmoid is exp(p) to all its digits.
+__device__ __forceinline__ float sigmoid(float p) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-p)));
+  if (p < -80.f) r = __expf(p);
+  return r;
+}
+
+// The filters of V neighbouring channels: V * K consecutive elements.
+template <typename T, int V, int K>
+__device__ __forceinline__ void load_taps(const T* wp, bool vec, float (&wf)[K][V]) {
+  float f[K * V];
+  if (vec) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) Vec<T, V>::load(wp + k * V, f + k * V);
+  } else {
+#pragma unroll
+    for (int i = 0; i < K * V; ++i) f[i] = to_f32(wp[i]);
+  }
+#pragma unroll
+  for (int c = 0; c < V; ++c)
+#pragma unroll
+    for (int k = 0; k < K; ++k) wf[k][c] = f[c * K + k];
+}
 
 // One thread: V channels, tt steps.  The thread of tile 0 alone reads and then
 // replaces the state of its channels, so the update in place has no race.
@@ -35,56 +64,56 @@ k_conv_fwd(ConvArgs a, const T* __restrict__ x, const T* __restrict__ w, const T
   const int h = hv / nv, c0 = (hv - h * nv) * V;
   const int L = seq_len(lengths, b, a.T);
   const int t0 = tile * a.tt, t1 = min(t0 + a.tt, a.T);
-  float wf[K][V], bf[V], win[K][V];  // win[K-1]: the step's own input
+  constexpr int U = 8;  // rows whose loads are in flight together
+  float wf[K][V], bf[V], win[K - 1 + U][V];
+  load_taps<T, V, K>(w + ((long long)h * a.d + c0) * K, a.wvec, wf);
 #pragma unroll
-  for (int c = 0; c < V; ++c) {
-    const T* wp = w + ((long long)h * a.d + c0 + c) * K;
-#pragma unroll
-    for (int k = 0; k < K; ++k) wf[k][c] = to_f32(wp[k]);
-    bf[c] = bias ? to_f32(bias[(long long)h * a.d + c0 + c]) : 0.f;
-  }
+  for (int c = 0; c < V; ++c) bf[c] = bias ? to_f32(bias[(long long)h * a.d + c0 + c]) : 0.f;
   const T* xp = x + row_off(a.sx, b, h, 0) + c0;
   T* yp = y + row_off(a.sy, b, h, 0) + c0;
   T* sp = state ? state + (((long long)b * a.H + h) * (K - 1)) * a.d + c0 : nullptr;
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) {
     const int t = t0 - (K - 1) + k;
-    if (t >= 0) {
-      if (t < L) Vec<T, V>::load(xp + t * a.sx.t, win[k + 1]);
-      else
-#pragma unroll
-        for (int c = 0; c < V; ++c) win[k + 1][c] = 0.f;
-    } else if (sp) {
-      Vec<T, V>::load(sp + (long long)(t + K - 1) * a.d, win[k + 1]);
+    if (t >= 0 && t < L) {
+      Vec<T, V>::load(xp + t * a.sx.t, win[k]);
+    } else if (t < 0 && sp) {
+      Vec<T, V>::load(sp + (long long)(t + K - 1) * a.d, win[k]);
     } else {
 #pragma unroll
-      for (int c = 0; c < V; ++c) win[k + 1][c] = 0.f;
+      for (int c = 0; c < V; ++c) win[k][c] = 0.f;
     }
   }
   const int te = min(t1, L);
-  constexpr int U = 4;  // rows whose loads are in flight together
-  for (int t = t0; t < te; t += U) {
-    float in[U][V];
+  auto step = [&](int u, T* to) {  // win[u + K - 1] is the step's own input
+    float out[V];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + u < te) Vec<T, V>::load(xp + (t + u) * a.sx.t, in[u]);
+    for (int c = 0; c < V; ++c) {
+      float p = bf[c];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (t + u < te) {
-        float out[V];
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-#pragma unroll
-          for (int k = 0; k < K - 1; ++k) win[k][c] = win[k + 1][c];
-          win[K - 1][c] = in[u][c];
-          float p = bf[c];
-#pragma unroll
-          for (int k = 0; k < K; ++k) p = fmaf(wf[k][c], win[k][c], p);
-          out[c] = SILU ? p / (1.f + __expf(-p)) : p;
-        }
-        Vec<T, V>::store(yp + (t + u) * a.sy.t, out);
-      }
+      for (int k = 0; k < K; ++k) p = fmaf(wf[k][c], win[u + k][c], p);
+      out[c] = SILU ? p * sigmoid(p) : p;
     }
+    Vec<T, V>::store(to, out);
+  };
+  auto shift = [&](int n) {
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+      for (int c = 0; c < V; ++c) win[k][c] = win[k + n][c];
+  };
+  int t = t0;
+  for (; t + U <= te; t += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) Vec<T, V>::load(xp + (t + u) * a.sx.t, win[K - 1 + u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) step(u, yp + (t + u) * a.sy.t);
+    shift(U);
+  }
+  for (; t < te; ++t) {
+    Vec<T, V>::load(xp + t * a.sx.t, win[K - 1]);
+    step(0, yp + t * a.sy.t);
+    shift(1);
   }
   if (te < t1) {  // steps behind the sequence's end
     float z[V];
@@ -107,6 +136,7 @@ k_conv_fwd(ConvArgs a, const T* __restrict__ x, const T* __restrict__ w, const T
 struct ConvBwdArgs {
   int B, H, T, d, tt, ntile;  // ntile: CTA tiles of kConvSub * tt steps
   int C;                      // H * d
+  int wvec;                   // filters can be read in pieces of V
   sdm_strides sx, sdy, sdx;
 };
 constexpr int kConvSub = 8;  // step sub-tiles of a CTA, summed in shared memory
@@ -128,20 +158,17 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
   const bool live = hv < a.H * nv;
   const int h = live ? hv / nv : 0, c0 = live ? (hv - h * nv) * V : 0;
   const int t0 = (tile * kConvSub + sub) * a.tt;
+  constexpr int U = 8;  // rows whose loads are in flight together
   float wf[K][V], bf[V], win[K][V], dpw[K][V], dw[K][V], db[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      wf[k][c] = live ? to_f32(w[((long long)h * a.d + c0 + c) * K + k]) : 0.f;
-      dw[k][c] = 0.f;
-      dpw[k][c] = 0.f;
-      win[k][c] = 0.f;
-    }
+    for (int k = 0; k < K; ++k) wf[k][c] = dw[k][c] = dpw[k][c] = win[k][c] = 0.f;
     bf[c] = bias && live ? to_f32(bias[(long long)h * a.d + c0 + c]) : 0.f;
     db[c] = 0.f;
   }
   if (live && t0 < a.T) {
+    load_taps<T, V, K>(w + ((long long)h * a.d + c0) * K, a.wvec, wf);
     const T* xp = x + row_off(a.sx, b, h, 0) + c0;
     const T* yp = dy + row_off(a.sdy, b, h, 0) + c0;
     T* op = dx + row_off(a.sdx, b, h, 0) + c0;
@@ -154,67 +181,84 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
     }
     const int own = min(t0 + a.tt, a.T);   // steps [t0, own) are this thread's
     const int end = own + K - 1;
-    constexpr int U = 4;
-    for (int tb = t0; tb < end; tb += U) {
+    // one step: input xi, gradient gi; `mine` counts in dw and db.  out: the gradient of
+    // input t - K + 1
+    auto step = [&](const float* xi, const float* gi, bool mine, float* out) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) {
+          win[k][c] = win[k + 1][c];
+          dpw[k][c] = dpw[k + 1][c];
+        }
+        win[K - 1][c] = xi[c];
+        float dp = gi[c];
+        if (SILU) {
+          float p = bf[c];
+#pragma unroll
+          for (int k = 0; k < K; ++k) p = fmaf(wf[k][c], win[k][c], p);
+          const float sg = sigmoid(p);
+          dp *= sg * fmaf(p, 1.f - sg, 1.f);
+        }
+        dpw[K - 1][c] = dp;
+        if (mine) {
+          db[c] += dp;
+#pragma unroll
+          for (int k = 0; k < K; ++k) dw[k][c] = fmaf(dp, win[k][c], dw[k][c]);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) s = fmaf(wf[k][c], dpw[K - 1 - k][c], s);
+        out[c] = s;
+      }
+    };
+    auto edge = [&](int t) {  // any step: range checks, states at both ends
+      float in[V], g[V], out[V];
+#pragma unroll
+      for (int c = 0; c < V; ++c) in[c] = g[c] = 0.f;
+      if (t < a.T) {
+        Vec<T, V>::load(xp + t * a.sx.t, in);
+        Vec<T, V>::load(yp + t * a.sdy.t, g);
+      }
+      step(in, g, t < own, out);
+      if (t >= a.T)  // behind the end dp is 0 whatever p is
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          dpw[K - 1][c] = 0.f;
+          out[c] = 0.f;
+#pragma unroll
+          for (int k = 1; k < K; ++k) out[c] = fmaf(wf[k][c], dpw[K - 1 - k][c], out[c]);
+        }
+      const int si = t - (K - 1);
+      if (si >= t0 || t0 == 0) {
+        const int r = si - a.T + K - 1;  // its row in the final state
+        if (dstate && r >= 0)
+#pragma unroll
+          for (int c = 0; c < V; ++c) out[c] += dstate[(st + r) * a.d + c0 + c];
+        if (si >= 0) Vec<T, V>::store(op + si * a.sdx.t, out);
+        else if (dstate0)
+#pragma unroll
+          for (int c = 0; c < V; ++c) dstate0[(st + si + K - 1) * a.d + c0 + c] = out[c];
+      }
+    };
+    int t = t0;
+    for (; t < min(t0 + K - 1, end); ++t) edge(t);
+    // steps whose input gradient is this thread's and meets neither end
+    for (; t + U <= own; t += U) {
       float in[U][V], g[U][V];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = tb + u;
-        if (t < end && t < a.T) {
-          Vec<T, V>::load(xp + t * a.sx.t, in[u]);
-          Vec<T, V>::load(yp + t * a.sdy.t, g[u]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < V; ++c) in[u][c] = g[u][c] = 0.f;
-        }
+        Vec<T, V>::load(xp + (t + u) * a.sx.t, in[u]);
+        Vec<T, V>::load(yp + (t + u) * a.sdy.t, g[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = tb + u;
-        if (t >= end) break;
-        const bool mine = t < own;
         float out[V];
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-#pragma unroll
-          for (int k = 0; k < K - 1; ++k) {
-            win[k][c] = win[k + 1][c];
-            dpw[k][c] = dpw[k + 1][c];
-          }
-          win[K - 1][c] = in[u][c];
-          float dp = g[u][c];
-          if (SILU) {
-            float p = bf[c];
-#pragma unroll
-            for (int k = 0; k < K; ++k) p = fmaf(wf[k][c], win[k][c], p);
-            const float sg = 1.f / (1.f + __expf(-p));
-            dp *= sg * fmaf(p, 1.f - sg, 1.f);
-            if (t >= a.T) dp = 0.f;
-          }
-          dpw[K - 1][c] = dp;
-          if (mine) {
-            db[c] += dp;
-#pragma unroll
-            for (int k = 0; k < K; ++k) dw[k][c] = fmaf(dp, win[k][c], dw[k][c]);
-          }
-          float s = 0.f;
-#pragma unroll
-          for (int k = 0; k < K; ++k) s = fmaf(wf[k][c], dpw[K - 1 - k][c], s);
-          out[c] = s;  // gradient of input t - K + 1
-        }
-        const int si = t - (K - 1);
-        if (si >= t0 || t0 == 0) {
-          const int r = si - a.T + K - 1;  // its row in the final state
-          if (dstate && r >= 0)
-#pragma unroll
-            for (int c = 0; c < V; ++c) out[c] += dstate[(st + r) * a.d + c0 + c];
-          if (si >= 0) Vec<T, V>::store(op + si * a.sdx.t, out);
-          else if (dstate0)
-#pragma unroll
-            for (int c = 0; c < V; ++c) dstate0[(st + si + K - 1) * a.d + c0 + c] = out[c];
-        }
+        step(in[u], g[u], true, out);
+        Vec<T, V>::store(op + (t + u - (K - 1)) * a.sdx.t, out);
       }
     }
+    for (; t < end; ++t) edge(t);
   }
   // sums over the CTA's sub-tiles, in order
   float* po = part + (size_t)blockIdx.y * (K + 1) * a.C;
@@ -268,13 +312,13 @@ static int conv_check(const sdm_conv_dims* d) {
   return SDM_OK;
 }
 
-// Steps a thread walks.  Longer tiles re-read fewer halo rows (K - 1 a tile,
-// from L2) and load the filter less often; shorter ones keep the card full.
-// 32 while that leaves four waves of resident threads, else down to 4.
+// Steps a thread walks.  Longer tiles re-read fewer halo rows (K - 1 a tile, from L2)
+// and load the filter less often; shorter ones keep the card full.  The longest that
+// still gives every SM 768 threads.
 static int conv_tile(const sdm_conv_dims* d, int V, int lo, int hi, int sub) {
   int tt = hi;
-  const long long vecs = (long long)d->B * d->H * (d->d / V);
-  while (tt > lo && vecs * (((long long)d->T + tt * sub - 1) / (tt * sub)) * sub < 4LL * 148 * 1024) tt >>= 1;
+  const long long vecs = (long long)d->B * d->H * ((d->d + V - 1) / V);
+  while (tt > lo && vecs * (((long long)d->T + tt * sub - 1) / (tt * sub)) * sub < 148LL * 768) tt >>= 1;
   return tt;
 }
 
@@ -316,7 +360,7 @@ static cudaError_t launch_conv_bwd(const ConvBwdArgs& a, bool silu, const void* 
 // Steps of a backward CTA's thread; the tile count of the grid's y axis stays
 // below its limit of 65535.
 static int conv_bwd_tiles(const sdm_conv_dims* d, int* tt) {
-  *tt = conv_tile(d, 4, 8, 64, kConvSub);
+  *tt = conv_tile(d, 2, 8, 64, kConvSub);
   long long n;
   while ((n = ((long long)d->T + *tt * kConvSub - 1) / (*tt * kConvSub)) * d->B > 65535 &&
          *tt < (1 << 26))
@@ -353,11 +397,12 @@ extern "C" int sdm_conv_forward(const void* x, const void* w, const void* bias, 
     if ((rc = need_ptr(p, es)) != SDM_OK) return rc;
   if (!aligned_to(bias, es) || !aligned_to(state_inout, es) || !aligned_to(lengths, 4))
     return SDM_ERR_ALIGN;
-  const int V = int(16 / es);
-  const bool vec = dims->d % V == 0 && view_aligned(x, *sx, es, 16) && view_aligned(y, *sy, es, 16) &&
-                   aligned_to(state_inout, 16);
-  ConvArgs a{dims->B, dims->H, dims->T, dims->d, 0, 0, *sx, *sy};
-  a.tt = conv_tile(dims, vec ? V : 1, 4, 32, 1);
+  const int V = 4;
+  const size_t vb = V * es;
+  const bool vec = dims->d % V == 0 && view_aligned(x, *sx, es, vb) && view_aligned(y, *sy, es, vb) &&
+                   aligned_to(state_inout, vb);
+  ConvArgs a{dims->B, dims->H, dims->T, dims->d, 0, 0, aligned_to(w, vb), *sx, *sy};
+  a.tt = conv_tile(dims, vec ? V : 1, 8, 64, 1);
   a.ntile = (dims->T + a.tt - 1) / a.tt;
   if (((long long)a.B * a.ntile * a.H * (a.d / (vec ? V : 1)) + 127) / 128 >= (1LL << 31))
     return SDM_ERR_DIMS;
@@ -366,7 +411,7 @@ extern "C" int sdm_conv_forward(const void* x, const void* w, const void* bias, 
   const cudaError_t e = conv_k(dims->K, [&](auto k) {
     constexpr int K = decltype(k)::value;
     if (bf)
-      return vec ? launch_conv_fwd<__nv_bfloat16, 8, K>(a, silu, x, w, bias, state_inout, lengths, y, s)
+      return vec ? launch_conv_fwd<__nv_bfloat16, 4, K>(a, silu, x, w, bias, state_inout, lengths, y, s)
                  : launch_conv_fwd<__nv_bfloat16, 1, K>(a, silu, x, w, bias, state_inout, lengths, y, s);
     return vec ? launch_conv_fwd<float, 4, K>(a, silu, x, w, bias, state_inout, lengths, y, s)
                : launch_conv_fwd<float, 1, K>(a, silu, x, w, bias, state_inout, lengths, y, s);
@@ -401,11 +446,12 @@ extern "C" int sdm_conv_backward(const void* x, const void* w, const void* bias,
     return SDM_ERR_ALIGN;
   if (!workspace || ws_bytes < sdm_conv_backward_workspace_bytes(dims)) return SDM_ERR_WORKSPACE;
   if (!aligned_to(workspace, 16)) return SDM_ERR_ALIGN;
-  const size_t vb = 4 * es;
-  const bool vec = dims->d % 4 == 0 && view_aligned(x, *sx, es, vb) &&
+  const size_t vb = 2 * es;
+  const bool vec = dims->d % 2 == 0 && view_aligned(x, *sx, es, vb) &&
                    view_aligned(dy, *sdy, es, vb) && view_aligned(dx, *sdx, es, vb) &&
                    aligned_to(state0, vb);
-  ConvBwdArgs a{dims->B, dims->H, dims->T, dims->d, 0, 0, dims->H * dims->d, *sx, *sdy, *sdx};
+  ConvBwdArgs a{dims->B, dims->H, dims->T, dims->d, 0, 0, dims->H * dims->d,
+                aligned_to(w, vb), *sx, *sdy, *sdx};
   a.ntile = conv_bwd_tiles(dims, &a.tt);
   if ((long long)a.B * a.ntile > 65535) return SDM_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -414,9 +460,9 @@ extern "C" int sdm_conv_backward(const void* x, const void* w, const void* bias,
   const cudaError_t e = conv_k(dims->K, [&](auto k) {
     constexpr int K = decltype(k)::value;
     if (bf)
-      return vec ? launch_conv_bwd<__nv_bfloat16, 4, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s)
+      return vec ? launch_conv_bwd<__nv_bfloat16, 2, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s)
                  : launch_conv_bwd<__nv_bfloat16, 1, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s);
-    return vec ? launch_conv_bwd<float, 4, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s)
+    return vec ? launch_conv_bwd<float, 2, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s)
                : launch_conv_bwd<float, 1, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s);
   });
   return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;

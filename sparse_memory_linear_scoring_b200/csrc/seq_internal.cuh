@@ -31,8 +31,14 @@ struct Vec {
   static __device__ __forceinline__ void load(const T* p, float* f) {
     if constexpr (V == 1) {
       f[0] = to_f32(*p);
+    } else if constexpr (V == 2 && sizeof(T) == 4) {
+      const float2 v = *reinterpret_cast<const float2*>(p);
+      f[0] = v.x; f[1] = v.y;
+    } else if constexpr (V == 2) {
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+      f[0] = __uint_as_float(u << 16); f[1] = __uint_as_float(u & 0xffff0000u);
     } else if constexpr (sizeof(T) == 4) {
-      static_assert(sizeof(T) != 4 || V == 4, "float vectors are 4 wide");
+      static_assert(sizeof(T) != 4 || V == 4, "float vectors are 2 or 4 wide");
       const float4 v = *reinterpret_cast<const float4*>(p);
       f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
     } else if constexpr (V == 8) {
@@ -52,6 +58,8 @@ struct Vec {
   static __device__ __forceinline__ void store(T* p, const float* f) {
     if constexpr (V == 1) {
       *p = from_f32<T>(f[0]);
+    } else if constexpr (V == 2 && sizeof(T) == 4) {
+      *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
     } else if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
     } else {
@@ -62,7 +70,8 @@ struct Vec {
         u[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
       if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-      else *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+      else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+      else *reinterpret_cast<uint32_t*>(p) = u[0];
     }
   }
 };
