@@ -21,14 +21,55 @@ struct ConvArgs {
   sdm_strides sx, sy;
 };
 
-// 1 / (1 + exp(-p)) with the reciprocal unit (2^-23 relative); its results below 2^-126
-// are flushed, and far below 0 the sigmoid is exp(p) to all its digits.
+// 1 / (1 + exp(-p)) on the special function unit, 2^-22 relative; 0 below p = -87.3,
+// where it is less than 2^-126.
 __device__ __forceinline__ float sigmoid(float p) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-p)));
-  if (p < -80.f) r = __expf(p);
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p * -kLog2e));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
+
+// acc += a * b over V channels, two to an instruction.
+template <int V>
+__device__ __forceinline__ void fma_row(float (&acc)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int c = 0; c < V; c += 2)
+      asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+          "mov.b64 z, {%0, %1};\n\tfma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+          : "+f"(acc[c]), "+f"(acc[c + 1]) : "f"(a[c]), "f"(a[c + 1]), "f"(b[c]), "f"(b[c + 1]));
+  } else {
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = fmaf(a[c], b[c], acc[c]);
+  }
+}
+
+// V elements as they lie in memory.
+template <typename T, int V>
+struct Raw {
+  uint32_t u[(V * sizeof(T) + 3) / 4];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (V * sizeof(T) == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+    } else if constexpr (V * sizeof(T) == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      u[0] = v.x; u[1] = v.y;
+    } else if constexpr (V * sizeof(T) == 4) {
+      u[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      u[0] = *reinterpret_cast<const unsigned short*>(p);
+    }
+  }
+  __device__ __forceinline__ void unpack(float* f) const {
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      if constexpr (sizeof(T) == 4) f[c] = __uint_as_float(u[c]);
+      else f[c] = __uint_as_float((c & 1) ? u[c / 2] & 0xffff0000u : u[c / 2] << 16);
+    }
+  }
+};
 
 // The filters of V neighbouring channels: V * K consecutive elements.
 template <typename T, int V, int K>
@@ -86,15 +127,16 @@ k_conv_fwd(ConvArgs a, const T* __restrict__ x, const T* __restrict__ w, const T
   }
   const int te = min(t1, L);
   auto step = [&](int u, T* to) {  // win[u + K - 1] is the step's own input
-    float out[V];
+    float p[V];
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      float p = bf[c];
+    for (int c = 0; c < V; ++c) p[c] = bf[c];
 #pragma unroll
-      for (int k = 0; k < K; ++k) p = fmaf(wf[k][c], win[u + k][c], p);
-      out[c] = SILU ? p * sigmoid(p) : p;
+    for (int k = 0; k < K; ++k) fma_row<V>(p, wf[k], win[u + k]);
+    if (SILU) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) p[c] *= sigmoid(p[c]);
     }
-    Vec<T, V>::store(to, out);
+    Vec<T, V>::store(to, p);
   };
   auto shift = [&](int n) {
 #pragma unroll
@@ -103,12 +145,26 @@ k_conv_fwd(ConvArgs a, const T* __restrict__ x, const T* __restrict__ w, const T
       for (int c = 0; c < V; ++c) win[k][c] = win[k + n][c];
   };
   int t = t0;
-  for (; t + U <= te; t += U) {
+  const int groups = te > t0 ? (te - t0) / U : 0;
+  if (groups > 0) {  // the next group's rows are on their way while one is computed
+    Raw<T, V> nx[U];
+    const T* xr = xp + t0 * a.sx.t;
+    T* yr = yp + t0 * a.sy.t;
+    auto fetch = [&]() {
 #pragma unroll
-    for (int u = 0; u < U; ++u) Vec<T, V>::load(xp + (t + u) * a.sx.t, win[K - 1 + u]);
+      for (int u = 0; u < U; ++u, xr += a.sx.t) nx[u].load(xr);
+    };
+    fetch();
+#pragma unroll 1
+    for (int n = 0; n < groups; ++n) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) step(u, yp + (t + u) * a.sy.t);
-    shift(U);
+      for (int u = 0; u < U; ++u) nx[u].unpack(win[K - 1 + u]);
+      if (n + 1 < groups) fetch();
+#pragma unroll
+      for (int u = 0; u < U; ++u, yr += a.sy.t) step(u, yr);
+      shift(U);
+    }
+    t += groups * U;
   }
   for (; t < te; ++t) {
     Vec<T, V>::load(xp + t * a.sx.t, win[K - 1]);
@@ -139,13 +195,13 @@ struct ConvBwdArgs {
   int wvec;                   // filters can be read in pieces of V
   sdm_strides sx, sdy, sdx;
 };
-constexpr int kConvSub = 8;  // step sub-tiles of a CTA, summed in shared memory
+constexpr int kConvSub = 4;  // step sub-tiles of a CTA, summed in shared memory
 
 // A CTA: 32 lanes of V channels x kConvSub sub-tiles of tt steps.  Each thread
 // recomputes p of its steps and of the K - 1 after them (their dp reaches back
 // into its tile).  part[b * ntile + tile][K + 1][C] gets the CTA's sums of dw, db.
 template <typename T, int V, int K, bool SILU>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kConvSub, K > 4 ? 1 : 4)
 k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
            const T* __restrict__ bias, const T* __restrict__ state0, const T* __restrict__ dy,
            const float* __restrict__ dstate, T* __restrict__ dx, float* __restrict__ dstate0,
@@ -158,7 +214,7 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
   const bool live = hv < a.H * nv;
   const int h = live ? hv / nv : 0, c0 = live ? (hv - h * nv) * V : 0;
   const int t0 = (tile * kConvSub + sub) * a.tt;
-  constexpr int U = 8;  // rows whose loads are in flight together
+  constexpr int U = 4;  // rows whose loads are in flight together
   float wf[K][V], bf[V], win[K][V], dpw[K][V], dw[K][V], db[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) {
@@ -183,7 +239,8 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
     const int end = own + K - 1;
     // one step: input xi, gradient gi; `mine` counts in dw and db.  out: the gradient of
     // input t - K + 1
-    auto step = [&](const float* xi, const float* gi, bool mine, float* out) {
+    auto step = [&](const float* xi, const float* gi, bool mine, float (&out)[V]) {
+      float dp[V];
 #pragma unroll
       for (int c = 0; c < V; ++c) {
 #pragma unroll
@@ -192,25 +249,33 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
           dpw[k][c] = dpw[k + 1][c];
         }
         win[K - 1][c] = xi[c];
-        float dp = gi[c];
-        if (SILU) {
-          float p = bf[c];
-#pragma unroll
-          for (int k = 0; k < K; ++k) p = fmaf(wf[k][c], win[k][c], p);
-          const float sg = sigmoid(p);
-          dp *= sg * fmaf(p, 1.f - sg, 1.f);
-        }
-        dpw[K - 1][c] = dp;
-        if (mine) {
-          db[c] += dp;
-#pragma unroll
-          for (int k = 0; k < K; ++k) dw[k][c] = fmaf(dp, win[k][c], dw[k][c]);
-        }
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) s = fmaf(wf[k][c], dpw[K - 1 - k][c], s);
-        out[c] = s;
+        dp[c] = gi[c];
       }
+      if (SILU) {
+        float p[V];
+#pragma unroll
+        for (int c = 0; c < V; ++c) p[c] = bf[c];
+#pragma unroll
+        for (int k = 0; k < K; ++k) fma_row<V>(p, wf[k], win[k]);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          const float sg = sigmoid(p[c]);
+          dp[c] *= fmaf(p[c] * sg, 1.f - sg, sg);
+        }
+      }
+      if (mine) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) db[c] += dp[c];
+#pragma unroll
+        for (int k = 0; k < K; ++k) fma_row<V>(dw[k], dp, win[k]);
+      }
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        dpw[K - 1][c] = dp[c];
+        out[c] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) fma_row<V>(out, wf[k], dpw[K - 1 - k]);
     };
     auto edge = [&](int t) {  // any step: range checks, states at both ends
       float in[V], g[V], out[V];
@@ -243,20 +308,39 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
     };
     int t = t0;
     for (; t < min(t0 + K - 1, end); ++t) edge(t);
-    // steps whose input gradient is this thread's and meets neither end
-    for (; t + U <= own; t += U) {
-      float in[U][V], g[U][V];
+    // steps whose input gradient is this thread's and meets neither end; the next group's
+    // rows are on their way while one is computed
+    const int groups = t < own ? (own - t) / U : 0;
+    if (groups > 0) {
+      Raw<T, V> nx[U], ng[U];
+      const T* xr = xp + t * a.sx.t;
+      const T* yr = yp + t * a.sdy.t;
+      T* orow = op + (t - (K - 1)) * a.sdx.t;
+      auto fetch = [&]() {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        Vec<T, V>::load(xp + (t + u) * a.sx.t, in[u]);
-        Vec<T, V>::load(yp + (t + u) * a.sdy.t, g[u]);
-      }
+        for (int u = 0; u < U; ++u, xr += a.sx.t, yr += a.sdy.t) {
+          nx[u].load(xr);
+          ng[u].load(yr);
+        }
+      };
+      fetch();
+#pragma unroll 1
+      for (int n = 0; n < groups; ++n) {
+        float in[U][V], g[U][V];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float out[V];
-        step(in[u], g[u], true, out);
-        Vec<T, V>::store(op + (t + u - (K - 1)) * a.sdx.t, out);
+        for (int u = 0; u < U; ++u) {
+          nx[u].unpack(in[u]);
+          ng[u].unpack(g[u]);
+        }
+        if (n + 1 < groups) fetch();
+#pragma unroll
+        for (int u = 0; u < U; ++u, orow += a.sdx.t) {
+          float out[V];
+          step(in[u], g[u], true, out);
+          Vec<T, V>::store(orow, out);
+        }
       }
+      t += groups * U;
     }
     for (; t < end; ++t) edge(t);
   }
@@ -267,7 +351,7 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
 #pragma unroll
     for (int c = 0; c < V; ++c) red[sub][lane][c] = k < K ? dw[k < K ? k : 0][c] : db[c];
     __syncthreads();
-    for (int j = threadIdx.x; j < 32 * V; j += 256) {
+    for (int j = threadIdx.x; j < 32 * V; j += 32 * kConvSub) {
       const int l = j / V, c = j - l * V;
       float s = 0.f;
 #pragma unroll
@@ -344,11 +428,11 @@ static cudaError_t launch_conv_bwd(const ConvBwdArgs& a, bool silu, const void* 
                                    float* dstate0, float* part, cudaStream_t s) {
   const dim3 grid((a.H * (a.d / V) + 31) / 32, a.B * a.ntile);
   if (silu)
-    k_conv_bwd<T, V, K, true><<<grid, 256, 0, s>>>(a, (const T*)x, (const T*)w, (const T*)bias,
+    k_conv_bwd<T, V, K, true><<<grid, 32 * kConvSub, 0, s>>>(a, (const T*)x, (const T*)w, (const T*)bias,
                                                    (const T*)state0, (const T*)dy, dstate, (T*)dx,
                                                    dstate0, part);
   else
-    k_conv_bwd<T, V, K, false><<<grid, 256, 0, s>>>(a, (const T*)x, (const T*)w, (const T*)bias,
+    k_conv_bwd<T, V, K, false><<<grid, 32 * kConvSub, 0, s>>>(a, (const T*)x, (const T*)w, (const T*)bias,
                                                     (const T*)state0, (const T*)dy, dstate,
                                                     (T*)dx, dstate0, part);
   cudaError_t e = cudaGetLastError();
@@ -360,7 +444,7 @@ static cudaError_t launch_conv_bwd(const ConvBwdArgs& a, bool silu, const void* 
 // Steps of a backward CTA's thread; the tile count of the grid's y axis stays
 // below its limit of 65535.
 static int conv_bwd_tiles(const sdm_conv_dims* d, int* tt) {
-  *tt = conv_tile(d, 2, 8, 64, kConvSub);
+  *tt = conv_tile(d, d->in_dtype == SDM_DTYPE_BF16 ? 4 : 2, 8, 64, kConvSub);
   long long n;
   while ((n = ((long long)d->T + *tt * kConvSub - 1) / (*tt * kConvSub)) * d->B > 65535 &&
          *tt < (1 << 26))
@@ -402,7 +486,7 @@ extern "C" int sdm_conv_forward(const void* x, const void* w, const void* bias, 
   const bool vec = dims->d % V == 0 && view_aligned(x, *sx, es, vb) && view_aligned(y, *sy, es, vb) &&
                    aligned_to(state_inout, vb);
   ConvArgs a{dims->B, dims->H, dims->T, dims->d, 0, 0, aligned_to(w, vb), *sx, *sy};
-  a.tt = conv_tile(dims, vec ? V : 1, 8, 64, 1);
+  a.tt = conv_tile(dims, vec ? V : 1, 8, 32, 1);
   a.ntile = (dims->T + a.tt - 1) / a.tt;
   if (((long long)a.B * a.ntile * a.H * (a.d / (vec ? V : 1)) + 127) / 128 >= (1LL << 31))
     return SDM_ERR_DIMS;
@@ -446,8 +530,9 @@ extern "C" int sdm_conv_backward(const void* x, const void* w, const void* bias,
     return SDM_ERR_ALIGN;
   if (!workspace || ws_bytes < sdm_conv_backward_workspace_bytes(dims)) return SDM_ERR_WORKSPACE;
   if (!aligned_to(workspace, 16)) return SDM_ERR_ALIGN;
-  const size_t vb = 2 * es;
-  const bool vec = dims->d % 2 == 0 && view_aligned(x, *sx, es, vb) &&
+  const int V = es == 2 ? 4 : 2;
+  const size_t vb = V * es;
+  const bool vec = dims->d % V == 0 && view_aligned(x, *sx, es, vb) &&
                    view_aligned(dy, *sdy, es, vb) && view_aligned(dx, *sdx, es, vb) &&
                    aligned_to(state0, vb);
   ConvBwdArgs a{dims->B, dims->H, dims->T, dims->d, 0, 0, dims->H * dims->d,
@@ -460,7 +545,7 @@ extern "C" int sdm_conv_backward(const void* x, const void* w, const void* bias,
   const cudaError_t e = conv_k(dims->K, [&](auto k) {
     constexpr int K = decltype(k)::value;
     if (bf)
-      return vec ? launch_conv_bwd<__nv_bfloat16, 2, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s)
+      return vec ? launch_conv_bwd<__nv_bfloat16, 4, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s)
                  : launch_conv_bwd<__nv_bfloat16, 1, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s);
     return vec ? launch_conv_bwd<float, 2, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s)
                : launch_conv_bwd<float, 1, K>(a, silu, x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, part, s);
