@@ -6,6 +6,8 @@
 // group's heads of q_h . kc_j = (sum_h q_h) . kc_j.  The list of a query at
 // position p: its own block c = p / block, then the best n_sel - 1 of the blocks
 // before it, higher score first and lower index at a tie, then -1.
+#include <limits.h>
+
 #include "block_internal.cuh"
 
 namespace sdm {
@@ -49,102 +51,212 @@ k_blk_pool(BlkArgs a, sdm_strides skc, const Tin* __restrict__ k, Tin* __restric
 }
 
 // ---------------------------------------------------------------- selection
-// Scores in double on CUDA cores: a rounding difference at a list's boundary
-// would change the list, and float sums differ from one order to the next by
-// more than neighbouring scores do about once in 10^5 rows.
-constexpr int kSelQ = 32;   // queries per CTA
-constexpr int kSelJ = 32;   // blocks per tile
+// Scores in double: a rounding difference at a list's boundary would change the list,
+// and float sums differ from one order to the next by more than neighbouring
+// scores do about once in 10^5 rows.  The products run on the double-precision tensor
+// instruction, which has the vector units' rate but takes a 16 x 8 x 16 product from 12
+// operands a lane, where a 2 x 2 tile of scalar products waits for shared memory
+// (8192 queries, 4 groups of d = 128, up to 128 blocks: 463 us that way, 2 batches).
+// A CTA takes 32 queries; its 8 warps score 16 queries x 32 blocks each, then a
+// warp per query extracts the best of its list and the 128 new scores, one at a
+// time: scores become ordered 64-bit integers, a lane keeps its own in descending
+// order, and the winner is the lane with the largest head.
+constexpr int kSelQ = 32;    // queries per CTA
+constexpr int kSelJ = 128;   // blocks per tile
 constexpr int kSelMost = 64;
+constexpr int kSelThreads = 256;
 
 __host__ __device__ inline size_t blk_select_smem(int d) {
-  // qs, kt [32][d + 1] double, scores [32][33] double, lists [32][64] (double, int)
-  return size_t(8) * (2 * 32 * (d + 1) + 32 * 33 + 32 * kSelMost) + size_t(4) * 32 * kSelMost;
+  // qs [32][d + 2] double, scores [32][129] double, lists [32][64] (64-bit key, int)
+  return size_t(8) * (kSelQ * (d + 2) + kSelQ * (kSelJ + 1) + kSelQ * kSelMost) + size_t(4) * kSelQ * kSelMost;
 }
 
-// Insert (s, j) into a descending list of m entries held in shared memory, all
-// lanes of the warp together; ls[m-1] < s on entry.
-__device__ __forceinline__ void list_insert(double* ls, int* li, int m, double s, int j) {
+// c += a b, 16 x 8 x 16.  With g = lane / 4, q = lane % 4: a[2 i + r] is row g + 8 r and
+// b[i] column g of inner index q + 4 i (any inner order, the same for both); c[0], c[1]
+// row g, columns 2 q, 2 q + 1, c[2], c[3] row g + 8.
+__device__ __forceinline__ void mma_f64(double (&c)[4], const double (&a)[8], const double (&b)[4]) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f64.f64.f64.f64 {%0,%1,%2,%3}, "
+               "{%4,%5,%6,%7,%8,%9,%10,%11}, {%12,%13,%14,%15}, {%0,%1,%2,%3};"
+               : "+d"(c[0]), "+d"(c[1]), "+d"(c[2]), "+d"(c[3])
+               : "d"(a[0]), "d"(a[1]), "d"(a[2]), "d"(a[3]), "d"(a[4]), "d"(a[5]), "d"(a[6]), "d"(a[7]),
+                 "d"(b[0]), "d"(b[1]), "d"(b[2]), "d"(b[3]));
+}
+
+// Order of scores as integers; 0 for -inf and NaN, which are never listed.
+__device__ __forceinline__ unsigned long long score_key(double s) {
+  s += 0.0;  // -0 ties with 0
+  if (!(s > -INFINITY)) return 0ull;
+  const unsigned long long u = __double_as_longlong(s);
+  return (u >> 63) ? ~u : u | (1ull << 63);
+}
+
+// Best m of the warp's candidates: NS keys a lane, with their blocks.  Writes them to
+// lk, li in order (lower block first at ties), the rest of the m places empty.
+template <int NS>
+__device__ __forceinline__ void extract_best(unsigned long long (&v)[NS], int (&id)[NS], int m,
+                                             unsigned long long* lk, int* li) {
   const int lane = threadIdx.x & 31;
-  const double a0 = lane < m ? ls[lane] : 0.0, a1 = lane + 32 < m ? ls[lane + 32] : 0.0;
-  const int i0 = lane < m ? li[lane] : 0, i1 = lane + 32 < m ? li[lane + 32] : 0;
-  const unsigned b0 = __ballot_sync(0xffffffffu, lane < m && a0 >= s);
-  const unsigned b1 = __ballot_sync(0xffffffffu, lane + 32 < m && a1 >= s);
-  const int pos = __popc(b0) + __popc(b1);
-  __syncwarp();
-  if (lane >= pos && lane + 1 < m) { ls[lane + 1] = a0; li[lane + 1] = i0; }
-  if (lane + 32 >= pos && lane + 33 < m) { ls[lane + 33] = a1; li[lane + 33] = i1; }
-  if (lane == 0) { ls[pos] = s; li[pos] = j; }
+  // descending, lower block first at ties (odd-even transposition: NS rounds)
+#pragma unroll
+  for (int r = 0; r < NS; ++r)
+#pragma unroll
+    for (int i = r & 1; i + 1 < NS; i += 2) {
+      const bool sw = v[i] < v[i + 1] || (v[i] == v[i + 1] && id[i] > id[i + 1]);
+      const unsigned long long a = sw ? v[i + 1] : v[i], b = sw ? v[i] : v[i + 1];
+      const int x = sw ? id[i + 1] : id[i], y = sw ? id[i] : id[i + 1];
+      v[i] = a; v[i + 1] = b;
+      id[i] = x; id[i + 1] = y;
+    }
+  int r = 0;
+  for (; r < m; ++r) {
+    const unsigned hi = unsigned(v[0] >> 32);
+    const unsigned top = __reduce_max_sync(0xffffffffu, hi);
+    if (top == 0) break;  // keys that are scores have a non-zero upper half
+    unsigned win = __ballot_sync(0xffffffffu, hi == top);
+    if (win & (win - 1)) {
+      const unsigned lo = hi == top ? unsigned(v[0]) : 0u;
+      const unsigned tl = __reduce_max_sync(0xffffffffu, lo);
+      const int j = hi == top && lo == tl ? id[0] : INT_MAX;
+      win = __ballot_sync(0xffffffffu, j == __reduce_min_sync(0xffffffffu, j));
+    }
+    if (win >> lane & 1) {
+      lk[r] = v[0];
+      li[r] = id[0];
+#pragma unroll
+      for (int i = 0; i + 1 < NS; ++i) {
+        v[i] = v[i + 1];
+        id[i] = id[i + 1];
+      }
+      v[NS - 1] = 0ull;
+    }
+  }
+  for (int e = r + lane; e < m; e += 32) {
+    lk[e] = 0ull;
+    li[e] = -1;
+  }
   __syncwarp();
 }
 
 template <typename Tin>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSelThreads)
 k_blk_select(BlkArgs a, sdm_strides skc, const Tin* __restrict__ q, const Tin* __restrict__ kc,
-             int nkc, int32_t* __restrict__ idx) {
+             int nkc, int32_t* __restrict__ idx, int vec) {
   extern __shared__ __align__(16) double sd[];
-  const int d = a.d, dp = d + 1, m = a.n_sel - 1;
+  const int d = a.d, dp = d + 2, m = a.n_sel - 1;  // pitch: 16-byte reads of 8 rows without conflicts
   double* qs = sd;
-  double* kt = qs + kSelQ * dp;
-  double* sc = kt + kSelJ * dp;
-  double* ls = sc + kSelQ * 33;
-  int* li = reinterpret_cast<int*>(ls + kSelQ * kSelMost);
+  double* sc = qs + kSelQ * dp;
+  unsigned long long* lk = reinterpret_cast<unsigned long long*>(sc + kSelQ * (kSelJ + 1));
+  int* li = reinterpret_cast<int*>(lk + kSelQ * kSelMost);
   const int nqt = (a.Tq + kSelQ - 1) / kSelQ;
   const int bg = blockIdx.x / nqt, q0 = (blockIdx.x - bg * nqt) * kSelQ;
   const int b = bg / a.G, g = bg - b * a.G;
   const int nq = min(kSelQ, a.Tq - q0), tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   const int p0 = blk_pos0(a, b) + q0;
-  for (int i = tid; i < kSelQ * d; i += 256) {
-    const int t = i / d, e = i - t * d;
-    double s = 0.0;
+  for (int i = tid; i < kSelQ * (d / 4); i += kSelThreads) {
+    const int t = i / (d / 4), e = (i - t * (d / 4)) * 4;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
     if (t < nq)
-      for (int r = 0; r < a.R; ++r) s += double(to_f32(q[row_off(a.sq, b, g * a.R + r, q0 + t) + e]));
-    qs[t * dp + e] = s;
-  }
-  for (int i = tid; i < kSelQ * kSelMost; i += 256) {
-    ls[i] = -INFINITY;
-    li[i] = -1;
+      for (int r = 0; r < a.R; ++r) {
+        const Tin* p = q + row_off(a.sq, b, g * a.R + r, q0 + t) + e;
+        float f[4];
+        if (vec & 1) {
+          Vec<Tin, 4>::load(p, f);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) f[u] = to_f32(p[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[u] += double(f[u]);
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) qs[t * dp + e + u] = s[u];
   }
   // blocks before the last query's own
   const int last = p0 + nq - 1;
   const int nj = m > 0 && last >= 0 ? min(last / a.bs, nkc) : 0;
+  const int qt = (wp & 1) * 16, jt = (wp >> 1) * 32, gr = lane >> 2, qd = lane & 3;
+  for (int i = tid; i < kSelQ * kSelMost && nj == 0; i += kSelThreads) li[i] = -1;
   for (int j0 = 0; j0 < nj; j0 += kSelJ) {
-    __syncthreads();
-    for (int i = tid; i < kSelJ * d; i += 256) {
-      const int j = i / d, e = i - j * d;
-      kt[j * dp + e] = j0 + j < nj ? double(to_f32(kc[row_off(skc, b, g, j0 + j) + e])) : 0.0;
-    }
-    __syncthreads();
-    {
-      const int t = (tid >> 4) * 2, j = tid & 15;
-      double s00 = 0, s01 = 0, s10 = 0, s11 = 0;
-      for (int e = 0; e < d; ++e) {
-        const double a0 = qs[t * dp + e], a1 = qs[(t + 1) * dp + e];
-        const double b0 = kt[j * dp + e], b1 = kt[(j + 16) * dp + e];
-        s00 = fma(a0, b0, s00); s01 = fma(a0, b1, s01);
-        s10 = fma(a1, b0, s10); s11 = fma(a1, b1, s11);
+    __syncthreads();  // the queries are in place; the last tile's scores have been read
+    if (qt < nq && j0 + jt < nj) {
+      double acc[4][4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0;
+      const Tin* kp[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)  // columns behind the last block repeat it and are not read back
+        kp[n] = kc + row_off(skc, b, g, min(j0 + jt + 8 * n + gr, nj - 1)) + 4 * qd;
+      for (int k = 0; k < d; k += 16) {
+        float f[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          if (vec & 2) {
+            Vec<Tin, 4>::load(kp[n] + k, f[n]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) f[n][u] = to_f32(kp[n][k + u]);
+          }
+        }
+        double af[8];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const double2* p = reinterpret_cast<const double2*>(qs + (qt + gr + 8 * r) * dp + k + 4 * qd);
+          const double2 x = p[0], y = p[1];
+          af[r] = x.x; af[2 + r] = x.y; af[4 + r] = y.x; af[6 + r] = y.y;
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const double bf[4] = {double(f[n][0]), double(f[n][1]), double(f[n][2]), double(f[n][3])};
+          mma_f64(acc[n], af, bf);
+        }
       }
-      sc[t * 33 + j] = s00; sc[t * 33 + j + 16] = s01;
-      sc[(t + 1) * 33 + j] = s10; sc[(t + 1) * 33 + j + 16] = s11;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        double* o = sc + (qt + gr) * (kSelJ + 1) + jt + 8 * n + 2 * qd;
+        o[0] = acc[n][0]; o[1] = acc[n][1];
+        o[8 * (kSelJ + 1)] = acc[n][2]; o[8 * (kSelJ + 1) + 1] = acc[n][3];
+      }
     }
     __syncthreads();
-    for (int t = wp; t < nq; t += 8) {
+    for (int t = wp; t < nq; t += kSelThreads / 32) {
       const int p = p0 + t;
-      const int cur = p >= 0 ? p / a.bs : 0;
-      const double s = sc[t * 33 + lane];
-      double* l = ls + t * kSelMost;
+      const int end = min(p >= 0 ? p / a.bs : 0, nj);  // blocks before the query's own
+      unsigned long long* l = lk + t * kSelMost;
       int* x = li + t * kSelMost;
-      // NaN compares false: such a block is never listed
-      unsigned todo = __ballot_sync(0xffffffffu, j0 + lane < min(cur, nj) && s > l[m - 1]);
-      while (todo) {
-        const int w = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const double sw = __shfl_sync(0xffffffffu, s, w);
-        if (sw > l[m - 1]) list_insert(l, x, m, sw, j0 + w);
+      unsigned long long v[4];
+      int id[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        id[c] = j0 + 32 * c + lane;
+        v[c] = id[c] < end ? score_key(sc[t * (kSelJ + 1) + 32 * c + lane]) : 0ull;
+      }
+      if (j0 == 0) {
+        extract_best<4>(v, id, m, l, x);
+      } else {
+        const unsigned long long worst = l[m - 1];  // a new block beats it or stays out
+        bool any = false;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) any |= v[c] > worst;
+        if (!__any_sync(0xffffffffu, any)) continue;
+        unsigned long long w[6];
+        int y[6];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) { w[c] = v[c]; y[c] = id[c]; }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int e = 32 * c + lane;
+          w[4 + c] = e < m ? l[e] : 0ull;
+          y[4 + c] = e < m ? x[e] : 0;
+        }
+        __syncwarp();
+        extract_best<6>(w, y, m, l, x);
       }
     }
   }
   __syncthreads();
-  for (int i = tid; i < nq * a.n_sel; i += 256) {
+  for (int i = tid; i < nq * a.n_sel; i += kSelThreads) {
     const int t = i / a.n_sel, r = i - t * a.n_sel, p = p0 + t;
     const int v = p < 0 ? -1 : (r == 0 ? p / a.bs : li[t * kSelMost + r - 1]);
     idx[((size_t)bg * a.Tq + q0) * a.n_sel + i] = v;
@@ -373,7 +485,9 @@ static cudaError_t launch_select(const BlkArgs& a, const sdm_strides& skc, const
   cudaError_t e = cudaFuncSetAttribute(k_blk_select<Tin>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(a.B * a.G) * unsigned((a.Tq + kSelQ - 1) / kSelQ);
-  k_blk_select<Tin><<<grid, 256, smem, s>>>(a, skc, (const Tin*)q, (const Tin*)kc, nkc, idx);
+  const int es = int(sizeof(Tin));
+  const int vec = (view_aligned(q, a.sq, es, 4 * es) ? 1 : 0) | (view_aligned(kc, skc, es, 4 * es) ? 2 : 0);
+  k_blk_select<Tin><<<grid, kSelThreads, smem, s>>>(a, skc, (const Tin*)q, (const Tin*)kc, nkc, idx, vec);
   return cudaGetLastError();
 }
 
