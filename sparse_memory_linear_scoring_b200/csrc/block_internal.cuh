@@ -11,12 +11,30 @@
 
 namespace sdm {
 
+// Division of 0 <= n < 2^31 by a fixed positive number: a multiply-high, an add and a
+// shift (with s = ceil(log2 d) and m = ceil(2^(32 + s) / d) - 2^32 it is exact).
+struct FastDiv {
+  uint32_t m, s, d;
+  __device__ __forceinline__ int div(int n) const {
+    return int((__umulhi(uint32_t(n), m) + uint32_t(n)) >> s);
+  }
+};
+inline FastDiv fast_div(int d) {
+  FastDiv f;
+  f.d = uint32_t(d);
+  f.s = 0;
+  while ((1ull << f.s) < f.d) ++f.s;
+  f.m = uint32_t(((1ull << (32 + f.s)) + f.d - 1) / f.d - (1ull << 32));
+  return f;
+}
+
 struct BlkArgs {
   int B, H, G, R;       // R = H / G heads per group
   int Tq, Tk, d, bs, n_sel;
   int nb;               // blocks, the last one possibly partial
   int q0, nq;           // queries of this pass: [q0, q0 + nq) of Tq
   float scale;
+  FastDiv by_R, by_sel;
   sdm_strides sq, sk, sv, so;
   const int32_t* lengths;
 };

@@ -63,24 +63,31 @@ k_blk_tile(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q,
     cp_async16(smem_u32(Ks + kk * L::LD + c), k + row_off(a.sk, b, grp, at) + c, in);
     cp_async16(smem_u32(Vs + kk * L::LD + c), v + row_off(a.sv, b, grp, at) + c, in);
   }
-  // rows of a tile: 16 per warp; lane l handles row l & 15 when fetching
-  auto fetch = [&](int base, int st) {
+  // rows of a tile: 16 per warp; lanes l and l + 16 know row l's keys (those it sees) and
+  // the place of its partial result
+  auto fetch = [&](int base, int st, int& keys, size_t& place) {
     __nv_bfloat16* dst = Qs + (st * kTileWarps + wp) * L::QW;
     const int row = base + 16 * wp + (lane & 15);
     const bool in = row < r1;
-    const int e = in ? entry[row / a.R] : 0;
-    const int h = grp * a.R + (in ? row % a.R : 0), t = a.q0 + e / a.n_sel;
-    const __nv_bfloat16* src = q + row_off(a.sq, b, h, t);
+    const int en = in ? a.by_R.div(row) : 0, r = in ? row - en * a.R : 0;
+    const int e = in ? entry[en] : 0;
+    const int t = a.q0 + a.by_sel.div(e);
+    keys = in ? min(BS, pos0 + t - k0 + 1) : 0;
+    place = ((size_t)bg * a.nq * a.n_sel + e) * a.R + r;
+    const unsigned long long src =
+        reinterpret_cast<unsigned long long>(q + row_off(a.sq, b, grp * a.R + r, t));
     // consecutive lanes take consecutive pieces of a row
+#pragma unroll
     for (int i = lane; i < 16 * (D / 8); i += 32) {
-      const int r = i / (D / 8), c = (i % (D / 8)) * 8;
-      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
-      const int ok = __shfl_sync(0xffffffffu, int(in), r);
-      cp_async16(smem_u32(dst + r * L::LD + c), p + c, ok != 0);
+      const int rr = i / (D / 8), c = (i % (D / 8)) * 8;
+      const __nv_bfloat16* p =
+          reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, src, rr));
+      cp_async16(smem_u32(dst + rr * L::LD + c), p + c, base + 16 * wp + rr < r1);
     }
   };
-  fetch(r0, 0);
+  int keys, nkeys = 0;
+  size_t place, nplace = 0;
+  fetch(r0, 0, keys, place);
   cp_async_commit();
   cp_async_wait<0>();
   __syncthreads();
@@ -101,27 +108,16 @@ k_blk_tile(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q,
 #pragma unroll
   for (int z = 0; z < BS / 32; ++z) anyodd |= odd[z];
   __half* part = static_cast<__half*>(w.part);
-  const float c2 = a.scale * kLog2e;
+  const float c2 = fabsf(a.scale) * kLog2e;
   const uint32_t ak = smem_u32(Ks), av = smem_u32(Vs);
 
-  for (int base = r0, st = 0; base < r1; base += kTileRows, st ^= 1) {
-    if (base + kTileRows < r1) fetch(base + kTileRows, st ^ 1);
+  for (int base = r0, st = 0; base < r1; base += kTileRows, st ^= 1, keys = nkeys, place = nplace) {
+    if (base + kTileRows < r1) fetch(base + kTileRows, st ^ 1, nkeys, nplace);
     cp_async_commit();
     __nv_bfloat16* mine = Qs + (st * kTileWarps + wp) * L::QW;
     const uint32_t aq = smem_u32(mine);
     const int ra = base + 16 * wp + g, rb = ra + 8;
-    int na = 0, nb = 0;  // keys the two rows see
-    size_t oa = 0, ob = 0;
-    if (ra < r1) {
-      const int e = entry[ra / a.R];
-      na = min(BS, pos0 + a.q0 + e / a.n_sel - k0 + 1);
-      oa = ((size_t)bg * a.nq * a.n_sel + e) * a.R + ra % a.R;
-    }
-    if (rb < r1) {
-      const int e = entry[rb / a.R];
-      nb = min(BS, pos0 + a.q0 + e / a.n_sel - k0 + 1);
-      ob = ((size_t)bg * a.nq * a.n_sel + e) * a.R + rb % a.R;
-    }
+    const int na = __shfl_sync(0xffffffffu, keys, g), nb = __shfl_sync(0xffffffffu, keys, g + 8);
     cp_async_wait<1>();
     __syncwarp();
     float sc[BS / 8][4];
@@ -141,29 +137,40 @@ k_blk_tile(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q,
         mma_bf16(sc[2 * n + 1], af, bf[2], bf[3]);
       }
     }
+    if (a.scale < 0.f) {
+#pragma unroll
+      for (int n = 0; n < BS / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[n][i] = -sc[n][i];
+    }
+    if (__any_sync(0xffffffffu, keys < BS)) {  // rows of the block's own queries, or none
+#pragma unroll
+      for (int n = 0; n < BS / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int col = 8 * n + 2 * qd + i;
+          if (col >= na) sc[n][i] = -INFINITY;
+          if (col >= nb) sc[n][2 + i] = -INFINITY;
+        }
+    }
     float ma = -INFINITY, mb = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < BS / 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = 8 * n + 2 * qd + i;
-        sc[n][i] = col < na ? sc[n][i] * c2 : -INFINITY;
-        sc[n][2 + i] = col < nb ? sc[n][2 + i] * c2 : -INFINITY;
-        ma = fmaxf(ma, sc[n][i]);
-        mb = fmaxf(mb, sc[n][2 + i]);
-      }
+    for (int n = 0; n < BS / 8; ++n) {
+      ma = fmaxf(ma, fmaxf(sc[n][0], sc[n][1]));
+      mb = fmaxf(mb, fmaxf(sc[n][2], sc[n][3]));
+    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
       mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     }
-    const float ba = ma == -INFINITY ? 0.f : ma, bb = mb == -INFINITY ? 0.f : mb;
+    const float ba = ma == -INFINITY ? 0.f : ma * c2, bb = mb == -INFINITY ? 0.f : mb * c2;
     float la = 0.f, lb = 0.f;
     uint32_t pf[BS / 16][4];
 #pragma unroll
     for (int n = 0; n < BS / 8; ++n) {
-      const float x0 = exp2f(sc[n][0] - ba), x1 = exp2f(sc[n][1] - ba);
-      const float x2 = exp2f(sc[n][2] - bb), x3 = exp2f(sc[n][3] - bb);
+      const float x0 = ex2(fmaf(sc[n][0], c2, -ba)), x1 = ex2(fmaf(sc[n][1], c2, -ba));
+      const float x2 = ex2(fmaf(sc[n][2], c2, -bb)), x3 = ex2(fmaf(sc[n][3], c2, -bb));
       la += x0 + x1;
       lb += x2 + x3;
       pf[n >> 1][(n & 1) * 2] = pack_bf16(x0, x1);
@@ -195,8 +202,8 @@ k_blk_tile(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q,
         // the weights of this lane's rows at 16 keys, one key at a time
         for (int y = 0; y < 16; ++y) {
           const int src = (lane & ~3) | ((y >> 1) & 3);
-          const uint32_t wa = __shfl_sync(0xffffffffu, pf[kk][(y >> 3) * 2], src);
-          const uint32_t wb = __shfl_sync(0xffffffffu, pf[kk][(y >> 3) * 2 + 1], src);
+          const uint32_t wa = __shfl_sync(0xffffffffu, y < 8 ? pf[kk][0] : pf[kk][2], src);
+          const uint32_t wb = __shfl_sync(0xffffffffu, y < 8 ? pf[kk][1] : pf[kk][3], src);
           const float xa = (y & 1) ? bf16_hi(wa) : bf16_lo(wa), xb = (y & 1) ? bf16_hi(wb) : bf16_lo(wb);
           const int key = 16 * kk + y;
 #pragma unroll
@@ -214,17 +221,22 @@ k_blk_tile(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q,
         }
       }
     }
-    // normalise, scale by the largest finite element, to halves
-    const float ia = la == 0.f ? 0.f : 1.f / la, ib = lb == 0.f ? 0.f : 1.f / lb;
+    // acc / la, scaled by the row's largest finite element, to halves
     float xa = 0.f, xb = 0.f;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int n = 0; n < D / 8; ++n) {
+      xa = fmaxf(xa, fmaxf(fabsf(acc[n][0]), fabsf(acc[n][1])));
+      xb = fmaxf(xb, fmaxf(fabsf(acc[n][2]), fabsf(acc[n][3])));
+    }
+    if (__any_sync(0xffffffffu, xa == INFINITY || xb == INFINITY)) {
+      xa = xb = 0.f;
+      for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float u = fabsf(acc[n][i] *= ia), z = fabsf(acc[n][2 + i] *= ib);
-        if (u < INFINITY) xa = fmaxf(xa, u);
-        if (z < INFINITY) xb = fmaxf(xb, z);
-      }
+        for (int i = 0; i < 2; ++i) {
+          if (fabsf(acc[n][i]) < INFINITY) xa = fmaxf(xa, fabsf(acc[n][i]));
+          if (fabsf(acc[n][2 + i]) < INFINITY) xb = fmaxf(xb, fabsf(acc[n][2 + i]));
+        }
+    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, o));
@@ -242,14 +254,16 @@ k_blk_tile(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q,
       *reinterpret_cast<__half2*>(stage + (g + 8) * L::LD + 8 * n + 2 * qd) =
           __floats2half2_rn(acc[n][2] * vb, acc[n][3] * vb);
     }
+    const size_t oa = __shfl_sync(0xffffffffu, place, g), ob = __shfl_sync(0xffffffffu, place, g + 8);
     if (qd == 0) {
-      if (ra < r1) w.ml[oa] = make_float2(la == 0.f ? -INFINITY : ba + log2f(la), xa);
-      if (rb < r1) w.ml[ob] = make_float2(lb == 0.f ? -INFINITY : bb + log2f(lb), xb);
+      if (ra < r1) w.ml[oa] = la == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(ba + log2f(la), xa / la);
+      if (rb < r1) w.ml[ob] = lb == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(bb + log2f(lb), xb / lb);
     }
     __syncwarp();
+#pragma unroll
     for (int i = lane; i < 16 * (D / 8); i += 32) {
       const int r = i / (D / 8), c = (i % (D / 8)) * 8;
-      const size_t o = r < 8 ? __shfl_sync(0xffffffffu, oa, (r & 7) * 4) : __shfl_sync(0xffffffffu, ob, (r & 7) * 4);
+      const size_t o = __shfl_sync(0xffffffffu, place, r);
       if (base + 16 * wp + r < r1)
         *reinterpret_cast<uint4*>(part + o * D + c) = *reinterpret_cast<const uint4*>(stage + r * L::LD + c);
     }
@@ -258,46 +272,71 @@ k_blk_tile(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q,
   cp_async_wait<0>();
 }
 
-// A row of o from its partials: D / 8 lanes a row.  The (query, slot) pairs without
-// keys have no partial and are skipped by the same test that left them out.
+// A row of o from its partials: D / 8 lanes a row.  A lane first takes every LN-th slot
+// of the list for the maximum and the sum, then each of LN slots at a time for its
+// weight, which the others get by shuffles, with 4 partial rows' loads in flight.  The
+// (query, slot) pairs without keys have no partial and are skipped by the same test
+// that left them out.
 template <int D>
 __global__ void __launch_bounds__(256)
 k_blk_join(BlkArgs a, BlkFwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ o,
            float* __restrict__ lse) {
   constexpr int LN = D / 8;
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
-  const int c = (threadIdx.x % LN) * 8;
-  if (i >= (long long)a.B * a.G * a.nq * a.R) return;
-  const int r = int(i % a.R);
-  const long long bt = i / a.R;
-  const int t = int(bt % a.nq), bg = int(bt / a.nq), b = bg / a.G, h = (bg - b * a.G) * a.R + r;
+  const int ln = threadIdx.x % LN, c = ln * 8;
+  const bool in = i < (long long)a.B * a.G * a.nq * a.R;
+  const long long i0 = in ? i : 0;
+  const long long bt = i0 / a.R;
+  const int r = int(i0 - bt * a.R);
+  const int bg = int(bt / a.nq), t = int(bt - (long long)bg * a.nq), b = bg / a.G, h = (bg - b * a.G) * a.R + r;
   const int32_t* list = idx + ((size_t)bg * a.Tq + a.q0 + t) * a.n_sel;
   const int p = blk_pos0(a, b) + a.q0 + t;
   const float2* ml = w.ml + (size_t)bt * a.n_sel * a.R + r;
   const __half* part = static_cast<const __half*>(w.part) + ((size_t)bt * a.n_sel * a.R + r) * D + c;
   float m = -INFINITY;
-  for (int s = 0; s < a.n_sel; ++s)
+  for (int s = ln; s < a.n_sel; s += LN)
     if (blk_keys(a, list[s], p) > 0) {
       const float x = ml[(size_t)s * a.R].x;
-      m = x != x ? x : fmaxf(m, x);
+      m = fmaxf(m, x);
     }
+#pragma unroll
+  for (int z = 1; z < LN; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.n_sel; ++s) {
-    if (blk_keys(a, list[s], p) == 0) continue;
-    const float2 u = ml[(size_t)s * a.R];
-    const uint4 x = *reinterpret_cast<const uint4*>(part + (size_t)s * a.R * D);
-    const float e = exp2f(u.x - base);
-    l += e;
-    const float f = e * u.y;
-    const __half2* hx = reinterpret_cast<const __half2*>(&x);
+  for (int s0 = 0; s0 < a.n_sel; s0 += LN) {
+    const int s = s0 + ln;
+    float f = -1.f;  // no partial
+    if (s < a.n_sel && blk_keys(a, list[s], p) > 0) {
+      const float2 u = ml[(size_t)s * a.R];
+      const float e = exp2f(u.x - base);
+      l += e;
+      f = e * u.y;
+    }
 #pragma unroll
-    for (int z = 0; z < 4; ++z) {
-      const float2 y = __half22float2(hx[z]);
-      acc[2 * z] = fmaf(f, y.x, acc[2 * z]);
-      acc[2 * z + 1] = fmaf(f, y.y, acc[2 * z + 1]);
+    for (int z0 = 0; z0 < LN; z0 += 4) {
+      uint4 x[4];
+      float fz[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        fz[z] = __shfl_sync(0xffffffffu, f, z0 + z, LN);
+        x[z] = make_uint4(0u, 0u, 0u, 0u);
+        if (fz[z] != -1.f) x[z] = *reinterpret_cast<const uint4*>(part + (size_t)(s0 + z0 + z) * a.R * D);
+      }
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const __half2* hx = reinterpret_cast<const __half2*>(&x[z]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 y = __half22float2(hx[u]);
+          acc[2 * u] = fmaf(fz[z], y.x, acc[2 * u]);
+          acc[2 * u + 1] = fmaf(fz[z], y.y, acc[2 * u + 1]);
+        }
+      }
     }
   }
+#pragma unroll
+  for (int z = 1; z < LN; z <<= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
+  if (!in) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int z = 0; z < 8; ++z) acc[z] *= inv;

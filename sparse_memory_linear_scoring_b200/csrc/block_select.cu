@@ -266,8 +266,8 @@ k_blk_select(BlkArgs a, sdm_strides skc, const Tin* __restrict__ q, const Tin* _
 // ---------------------------------------------------------------- plan
 // Counting sort by block.  Each segment of queries counts its pairs per block;
 // one CTA per (b, group) turns the counts into first positions, block by block and
-// segment by segment; then each segment places its pairs, one warp walking them in
-// order, so the lists come out in query order whatever runs first.
+// segment by segment; then each segment places its pairs, its warps walking their
+// shares in order, so the lists come out in query order whatever runs first.
 __global__ void __launch_bounds__(256)
 k_blk_count(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
   extern __shared__ int cnt[];
@@ -279,7 +279,7 @@ k_blk_count(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
   const int32_t* ip = idx + ((size_t)bg * a.Tq + a.q0 + q0) * a.n_sel;
   for (int i = threadIdx.x; i < n; i += 256) {
     const int j = ip[i];
-    if (blk_keys(a, j, pos0 + a.q0 + q0 + i / a.n_sel) > 0) atomicAdd(&cnt[j], 1);
+    if (blk_keys(a, j, pos0 + a.q0 + q0 + a.by_sel.div(i)) > 0) atomicAdd(&cnt[j], 1);
   }
   __syncthreads();
   int* o = p.hist + (size_t)blockIdx.x * a.nb;
@@ -340,32 +340,55 @@ k_blk_offsets(BlkArgs a, BlkPlan p) {
   }
 }
 
-__global__ void __launch_bounds__(32)
-k_blk_place(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
-  extern __shared__ int at[];
-  const int sg = blockIdx.x % p.nseg, bg = blockIdx.x / p.nseg, lane = threadIdx.x;
+// W warps share a segment: each counts its part of the pairs, the counts become
+// first positions warp by warp, and each places its part.
+__global__ void __launch_bounds__(256)
+k_blk_place(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx, int W) {
+  extern __shared__ int at[];  // [W][nb]
+  const int sg = blockIdx.x % p.nseg, bg = blockIdx.x / p.nseg;
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, nt = 32 * W;
   const int* h = p.hist + (size_t)blockIdx.x * a.nb;
-  for (int j = lane; j < a.nb; j += 32) at[j] = h[j];
-  __syncwarp();
+  for (int i = threadIdx.x; i < W * a.nb; i += nt) at[i] = 0;
+  __syncthreads();
   const int pos0 = blk_pos0(a, bg / a.G);
   const int q0 = sg * p.seg, n = min(p.seg, a.nq - q0) * a.n_sel;
   const int32_t* ip = idx + ((size_t)bg * a.Tq + a.q0 + q0) * a.n_sel;
   int* out = p.entry + (size_t)bg * a.nq * a.n_sel;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int i = i0 + lane;
-    int j = -1;
-    if (i < n) {
-      j = ip[i];
-      if (blk_keys(a, j, pos0 + a.q0 + q0 + i / a.n_sel) == 0) j = -1;
+  const int each = ((n + W - 1) / W + 31) & ~31;
+  const int i1 = min(n, (wp + 1) * each);
+  int* mine = at + (size_t)wp * a.nb;
+  auto block_of = [&](int i) {
+    if (i >= i1) return -1;
+    const int j = ip[i];
+    return blk_keys(a, j, pos0 + a.q0 + q0 + a.by_sel.div(i)) > 0 ? j : -1;
+  };
+  if (W > 1) {
+    for (int i = wp * each + lane; i < i1; i += 32) {
+      const int j = block_of(i);
+      if (j >= 0) atomicAdd(&mine[j], 1);
     }
+    __syncthreads();
+  }
+  for (int j = threadIdx.x; j < a.nb; j += nt) {
+    int x = h[j];
+    for (int w = 0; w < W; ++w) {
+      const int c = at[(size_t)w * a.nb + j];
+      at[(size_t)w * a.nb + j] = x;
+      x += c;
+    }
+  }
+  __syncthreads();
+  for (int i0 = wp * each; i0 < i1; i0 += 32) {
+    const int i = i0 + lane;
+    const int j = block_of(i);
     const unsigned same = __match_any_sync(0xffffffffu, j);
     const int rank = __popc(same & ((1u << lane) - 1));
     int base = 0;
-    if (j >= 0) base = at[j];
+    if (j >= 0) base = mine[j];
     __syncwarp();
     if (j >= 0) {
       out[base + rank] = q0 * a.n_sel + i;
-      if (rank == 0) at[j] = base + __popc(same);
+      if (rank == 0) mine[j] = base + __popc(same);
     }
     __syncwarp();
   }
@@ -401,14 +424,16 @@ BlkPlan blk_plan(const sdm_block_dims* d, int nq, int rows, void* base) {
 
 cudaError_t launch_blk_plan(const BlkArgs& a, const BlkPlan& p, const int32_t* idx, cudaStream_t s) {
   const int smem = a.nb * 4;
+  int W = 8;  // warps of a segment, as many as its counts leave room for
+  while (W > 1 && (W * smem > 64 * 1024)) W >>= 1;
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(k_blk_count, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(k_blk_place, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+      (e = cudaFuncSetAttribute(k_blk_place, cudaFuncAttributeMaxDynamicSharedMemorySize, W * smem)) != cudaSuccess)
     return e;
   const unsigned grid = unsigned(a.B * a.G) * unsigned(p.nseg);
   k_blk_count<<<grid, 256, smem, s>>>(a, p, idx);
   k_blk_offsets<<<a.B * a.G, 1024, 0, s>>>(a, p);
-  k_blk_place<<<grid, 32, smem, s>>>(a, p, idx);
+  k_blk_place<<<grid, 32 * W, W * smem, s>>>(a, p, idx, W);
   return cudaGetLastError();
 }
 
@@ -445,6 +470,8 @@ BlkArgs blk_args(const sdm_block_dims* d, const sdm_block_views* v, const int32_
   a.nb = (d->Tk + d->block - 1) / d->block;
   a.q0 = 0; a.nq = d->Tq;
   a.scale = d->scale;
+  a.by_R = fast_div(a.R);
+  a.by_sel = fast_div(a.n_sel);
   a.sq = v->q; a.sk = v->k; a.sv = v->v; a.so = v->o;
   a.lengths = lengths;
   return a;

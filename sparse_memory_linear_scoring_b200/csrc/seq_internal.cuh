@@ -103,6 +103,13 @@ __device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T) {
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
+// 2^x on the special function unit; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
