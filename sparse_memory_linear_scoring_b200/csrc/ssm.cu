@@ -18,15 +18,22 @@ namespace sdm {
 // Forward: segS[i] := state before segment i, S_end := the last state.
 // Reverse: segS[i] := gradient arriving at the end of segment i (from S0, the
 // gradient of the last state, or 0), S_end := gradient of the first state.
-__global__ void __launch_bounds__(256)
-k_ssm_carry(float* __restrict__ segS, const float* __restrict__ segG, const float* S0, float* S_end,
-            int nseg, int PN, int reverse) {
+struct Carry {
+  float* segS;
+  const float* S0;
+  float* S_end;
+  int reverse;
+};
+
+__global__ void __launch_bounds__(128)
+k_ssm_carry(Carry c0, Carry c1, const float* __restrict__ segG, int nseg, int PN) {
+  const Carry c = blockIdx.z ? c1 : c0;
   const int bh = blockIdx.y;
-  const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int e = (blockIdx.x * 128 + threadIdx.x) * 4;
   if (e >= PN) return;
-  float4 S = S0 ? *reinterpret_cast<const float4*>(S0 + (size_t)bh * PN + e)
-                : make_float4(0.f, 0.f, 0.f, 0.f);
-  float* p = segS + (size_t)bh * nseg * PN + e;
+  float4 S = c.S0 ? *reinterpret_cast<const float4*>(c.S0 + (size_t)bh * PN + e)
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+  float* p = c.segS + (size_t)bh * nseg * PN + e;
   const float* g = segG + (size_t)bh * nseg;
   constexpr int U = 8;  // segments whose loads are in flight together
   for (int i0 = 0; i0 < nseg; i0 += U) {
@@ -35,7 +42,7 @@ k_ssm_carry(float* __restrict__ segS, const float* __restrict__ segG, const floa
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i0 + u < nseg) {
-        const int i = reverse ? nseg - 1 - (i0 + u) : i0 + u;
+        const int i = c.reverse ? nseg - 1 - (i0 + u) : i0 + u;
         v[u] = *reinterpret_cast<const float4*>(p + (size_t)i * PN);
         d[u] = g[i];
       }
@@ -43,7 +50,7 @@ k_ssm_carry(float* __restrict__ segS, const float* __restrict__ segG, const floa
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i0 + u < nseg) {
-        const int i = reverse ? nseg - 1 - (i0 + u) : i0 + u;
+        const int i = c.reverse ? nseg - 1 - (i0 + u) : i0 + u;
         *reinterpret_cast<float4*>(p + (size_t)i * PN) = S;
         const float a = exp2f(d[u]);
         S.x = fmaf(a, S.x, v[u].x); S.y = fmaf(a, S.y, v[u].y);
@@ -51,19 +58,32 @@ k_ssm_carry(float* __restrict__ segS, const float* __restrict__ segG, const floa
       }
     }
   }
-  if (S_end) *reinterpret_cast<float4*>(S_end + (size_t)bh * PN + e) = S;
+  if (c.S_end) *reinterpret_cast<float4*>(c.S_end + (size_t)bh * PN + e) = S;
 }
 
-cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, float* S_end, int BH,
-                             int nseg, int PN, bool reverse, cudaStream_t s) {
+static cudaError_t launch_carry(const Carry& c0, const Carry& c1, int both, const float* segG, int BH,
+                                int nseg, int PN, cudaStream_t s) {
   for (int b0 = 0; b0 < BH; b0 += 65535) {  // the grid's y axis ends at 65535
     const int n = BH - b0 < 65535 ? BH - b0 : 65535;
     const size_t o = size_t(b0) * PN;
-    k_ssm_carry<<<dim3((PN / 4 + 255) / 256, n), 256, 0, s>>>(
-        segS + size_t(b0) * nseg * PN, segG + size_t(b0) * nseg, S0 ? S0 + o : nullptr,
-        S_end ? S_end + o : nullptr, nseg, PN, reverse ? 1 : 0);
+    auto at = [&](const Carry& c) {
+      return Carry{c.segS + o * nseg, c.S0 ? c.S0 + o : nullptr, c.S_end ? c.S_end + o : nullptr, c.reverse};
+    };
+    k_ssm_carry<<<dim3((PN / 4 + 127) / 128, n, both ? 2 : 1), 128, 0, s>>>(
+        at(c0), at(c1), segG + size_t(b0) * nseg, nseg, PN);
   }
   return cudaGetLastError();
+}
+
+cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, int BH, int nseg, int PN,
+                             cudaStream_t s) {
+  const Carry c = {segS, S0, nullptr, 0};
+  return launch_carry(c, c, 0, segG, BH, nseg, PN, s);
+}
+
+cudaError_t launch_ssm_carries(float* fS, float* gS, const float* lg, const float* S0, float* ST,
+                               const float* dST, float* dS0, int BH, int nch, int PN, cudaStream_t s) {
+  return launch_carry({fS, S0, ST, 0}, {gS, dST, dS0, 1}, 1, lg, BH, nch, PN, s);
 }
 
 // ---------------------------------------------------------------- CUDA-core walk
@@ -307,15 +327,18 @@ int ssm_check(const sdm_ssm_dims* d) {
   return SDM_OK;
 }
 
-// Segments: enough that (head, segment) pairs fill the card twice over, of at
-// least 4 chunks each so that the first pass and the carry stay small beside the
-// walk (a segment's state costs as many bytes as its x over P N / (P Q) chunks).
+// Segments: enough that (head, segment) pairs fill the card twice over, but few enough
+// that the carry, about 0.1 us a segment of a head, stays below the two walks of 2 to 5 us
+// a chunk: 2 c nch / nseg + 0.1 nseg is least near nseg = 8 sqrt(nch).  (At least 4 chunks
+// a segment, as a rule on the states' bytes would have it, cost 777 steps of 3 float32
+// heads 57 us in the walks instead of 16.)
 static void ssm_segments(const sdm_ssm_dims* d, int Q, SsmArgs* a) {
   a->Q = Q;
   a->nch = (d->T + Q - 1) / Q;
   const long long BH = (long long)d->B * d->H;
   long long nseg = (2 * 148 + BH - 1) / BH;
-  if (nseg > a->nch / 4) nseg = a->nch / 4;
+  while (nseg > 1 && nseg * nseg > 64LL * a->nch) --nseg;
+  if (nseg > a->nch) nseg = a->nch;
   if (nseg < 1) nseg = 1;
   a->cps = int((a->nch + nseg - 1) / nseg);
   if (a->cps < 1) a->cps = 1;
@@ -354,7 +377,7 @@ static cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, const void* x, const fl
     k_ssm_walk<Tin, false><<<grid, kWalkThreads, smem, s>>>(
         a, (const Tin*)x, dt, A, (const Tin*)Bm, (const Tin*)Cm, D, S, lengths, (Tin*)y, segS, segG);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_ssm_carry(segS, segG, S, nullptr, a.B * a.H, a.nseg, a.P * a.N, false, s)) !=
+    if ((e = launch_ssm_carry(segS, segG, S, a.B * a.H, a.nseg, a.P * a.N, s)) !=
         cudaSuccess)
       return e;
   }

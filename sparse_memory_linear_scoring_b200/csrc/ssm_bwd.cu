@@ -27,22 +27,6 @@ namespace sdm {
 
 constexpr int kBwdThreads = 256;
 
-struct SsmBwdArgs {
-  SsmArgs a;  // sy: strides of dy
-  sdm_strides sdx, sddt, sdB, sdC;
-};
-
-struct SsmBwdWs {
-  float* fS;    // [BH][nch][P][N] state before each chunk
-  float* gS;    // [BH][nch][P][N] gradient arriving at each chunk's end
-  float* ST;    // [BH][P][N] last state
-  float* lg;    // [BH][nch] log2 decay of each chunk
-  float* dAD;   // [BH][nch][2] parts of dA and dD
-  float* pB;    // [BH][T][N] per-head dB, dC where heads share them
-  float* pC;
-  size_t total;
-};
-
 static SsmBwdWs ssm_bwd_ws(const sdm_ssm_dims* d, int Q, void* base) {
   SsmBwdWs w;
   memset(&w, 0, sizeof(w));
@@ -431,8 +415,7 @@ static cudaError_t launch_ssm_bwd_simt(const SsmBwdArgs& ba, const void* x, cons
                                                  (const Tin*)Cm, (const Tin*)dy, w.fS, w.gS, w.lg);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int BH = a.B * a.H, PN = a.P * a.N;
-  if ((e = launch_ssm_carry(w.fS, w.lg, S0, w.ST, BH, a.nch, PN, false, s)) != cudaSuccess) return e;
-  if ((e = launch_ssm_carry(w.gS, w.lg, dST, dS0, BH, a.nch, PN, true, s)) != cudaSuccess) return e;
+  if ((e = launch_ssm_carries(w.fS, w.gS, w.lg, S0, w.ST, dST, dS0, BH, a.nch, PN, s)) != cudaSuccess) return e;
   k_ssm_bwd<Tin><<<grid, kBwdThreads, s2, s>>>(ba, (const Tin*)x, dt, A, (const Tin*)Bm,
                                                (const Tin*)Cm, D, (const Tin*)dy, w, (Tin*)dx, ddt,
                                                (Tin*)dB, (Tin*)dC);
@@ -459,7 +442,7 @@ static long long ssm_bwd_grid(const sdm_ssm_dims* d) {
 
 extern "C" size_t sdm_ssm_backward_workspace_bytes(const sdm_ssm_dims* dims) {
   if (ssm_check(dims) != SDM_OK || ssm_bwd_grid(dims) >= (1LL << 31)) return 0;
-  const size_t n = ssm_bwd_ws(dims, kSsmQ, nullptr).total;
+  size_t n = ssm_bwd_ws(dims, kSsmQ, nullptr).total;  // the shorter chunks need more
   return n > 0 ? n : 16;
 }
 
@@ -487,12 +470,17 @@ extern "C" int sdm_ssm_backward(const void* x, const float* dt, const float* A, 
   SsmBwdArgs ba;
   ba.a = ssm_args(dims, views);
   ba.sdx = grad_views->x; ba.sddt = grad_views->dt; ba.sdB = grad_views->B; ba.sdC = grad_views->C;
-  ba.a.Q = kSsmQ;
-  ba.a.nch = (dims->T + kSsmQ - 1) / kSsmQ;
-  const SsmBwdWs w = ssm_bwd_ws(dims, kSsmQ, workspace);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = dims->in_dtype == SDM_DTYPE_BF16;
-  cudaError_t e = bf ? launch_ssm_bwd_simt<__nv_bfloat16>(ba, x, dt, A, Bm, Cm, D, S0, dy, dS_T, w, dx, ddt, dB, dC, dS0, s)
+  const bool mma = ssm_tensor_sizes(dims) && view_aligned(x, ba.a.sx, 2, 16) &&
+                   view_aligned(Bm, ba.a.sB, 2, 16) && view_aligned(Cm, ba.a.sC, 2, 16) &&
+                   view_aligned(dy, ba.a.sy, 2, 16) && view_aligned(dx, ba.sdx, 2, 4) &&
+                   view_aligned(dB, ba.sdB, 2, 4) && view_aligned(dC, ba.sdC, 2, 4);
+  ba.a.Q = mma ? kSsmQT : kSsmQ;
+  ba.a.nch = (dims->T + ba.a.Q - 1) / ba.a.Q;
+  const SsmBwdWs w = ssm_bwd_ws(dims, ba.a.Q, workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = mma ? launch_ssm_bwd_mma(ba, x, dt, A, Bm, Cm, D, S0, dy, dS_T, w, dx, ddt, dB, dC, dS0, s)
+                : bf ? launch_ssm_bwd_simt<__nv_bfloat16>(ba, x, dt, A, Bm, Cm, D, S0, dy, dS_T, w, dx, ddt, dB, dC, dS0, s)
                      : launch_ssm_bwd_simt<float>(ba, x, dt, A, Bm, Cm, D, S0, dy, dS_T, w, dx, ddt, dB, dC, dS0, s);
   if (e == cudaSuccess)
     e = bf ? launch_ssm_fold<__nv_bfloat16>(ba, w, dB, dC, s) : launch_ssm_fold<float>(ba, w, dB, dC, s);

@@ -1,5 +1,5 @@
 // ssm_internal.cuh -- the selective state space scan (ssm.cu, ssm_mma.cu,
-// ssm_bwd.cu): sizes of a call, its workspace, and what the kernels share.
+// ssm_bwd.cu, ssm_bwd_mma.cu): sizes of a call, its workspace, and what the kernels share.
 //
 // Per (b,h) head, S in R^{P x N} (P = d_v rows, N = d_k columns as in gdn.cu):
 //     a_t = exp(dt_t A_h);  S_t = a_t S_{t-1} + dt_t x_t B_t^T;  y_t = S_t C_t + D_h x_t,
@@ -68,8 +68,8 @@ __device__ __forceinline__ float decay_between(float hi_t, float lo_t, float hi_
 // Launchers.  The states kernel writes, per (head, segment), the segment's own
 // contribution to the state and its total log2 decay; the carry kernel turns the
 // former into the state before each segment.
-cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, float* S_end, int BH,
-                             int nseg, int PN, bool reverse, cudaStream_t s);
+cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, int BH, int nseg, int PN,
+                             cudaStream_t s);
 
 // The tensor-core walk takes bf16 inputs of widths 64 and 128 whose views allow
 // 16-byte pieces.
@@ -80,6 +80,32 @@ cudaError_t launch_ssm_fwd_mma(const SsmArgs& a, const void* x, const float* dt,
 inline bool ssm_tensor_sizes(const sdm_ssm_dims* d) {
   return d->in_dtype == SDM_DTYPE_BF16 && d->d_v >= 64 && d->d_k >= 64;
 }
+
+// Backward pass (ssm_bwd.cu, ssm_bwd_mma.cu).
+struct SsmBwdArgs {
+  SsmArgs a;  // sy: strides of dy
+  sdm_strides sdx, sddt, sdB, sdC;
+};
+
+struct SsmBwdWs {
+  float* fS;    // [BH][nch][P][N] state before each chunk
+  float* gS;    // [BH][nch][P][N] gradient arriving at each chunk's end
+  float* ST;    // [BH][P][N] last state
+  float* lg;    // [BH][nch] log2 decay of each chunk
+  float* dAD;   // [BH][nch][2] parts of dA and dD
+  float* pB;    // [BH][T][N] per-head dB, dC where heads share them
+  float* pC;
+  size_t total;
+};
+
+// Both carries of the backward pass in one launch: states before the chunks and last
+// states from S0, gradients at the chunks' ends and of S0 from dST.
+cudaError_t launch_ssm_carries(float* fS, float* gS, const float* lg, const float* S0, float* ST,
+                               const float* dST, float* dS0, int BH, int nch, int PN, cudaStream_t s);
+cudaError_t launch_ssm_bwd_mma(const SsmBwdArgs& ba, const void* x, const float* dt, const float* A,
+                               const void* Bm, const void* Cm, const float* D, const float* S0,
+                               const void* dy, const float* dST, const SsmBwdWs& w, void* dx, float* ddt,
+                               void* dB, void* dC, float* dS0, cudaStream_t s);
 
 // Argument checks and sizes shared by the entry points.
 SsmArgs ssm_args(const sdm_ssm_dims* d, const sdm_ssm_views* v);

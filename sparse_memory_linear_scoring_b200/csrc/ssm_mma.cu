@@ -297,7 +297,7 @@ static cudaError_t launch_tile(const SsmArgs& a, const void* x, const float* dt,
     k_ssm_tile<P, N, false><<<grid, P * 2, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm,
                                                    D, S, lengths, (bf*)y, segS, segG);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_ssm_carry(segS, segG, S, nullptr, a.B * a.H, a.nseg, P * N, false, s)) != cudaSuccess)
+    if ((e = launch_ssm_carry(segS, segG, S, a.B * a.H, a.nseg, P * N, s)) != cudaSuccess)
       return e;
   }
   const int sm = int(SsmTile<P, N, true>::smem);
