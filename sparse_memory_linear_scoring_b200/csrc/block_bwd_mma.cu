@@ -69,24 +69,36 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     cp_async16(smem_u32(Ks + kk * L::LD + c), k + row_off(a.sk, b, grp, at) + c, in);
     cp_async16(smem_u32(Vs + kk * L::LD + c), v + row_off(a.sv, b, grp, at) + c, in);
   }
-  auto fetch = [&](int base, int st) {  // the warp's own 16 rows of Q and dO
+  // the warp's own 16 rows of Q and dO; lanes l and l + 16 know row l: the keys it sees,
+  // the place of its part of dq, log2 of its softmax sum and its delta
+  struct Row { int keys; size_t place; float l2, dl; };
+  auto fetch = [&](int base, int st, Row& me) {
     __nv_bfloat16* dq_ = Rs + st * 2 * L::RW + wp * 16 * L::LD;
     const int row = base + 16 * wp + (lane & 15);
     const bool in = row < r1;
-    const int e = in ? entry[row / a.R] : 0;
-    const int h = grp * a.R + (in ? row % a.R : 0), t = a.q0 + e / a.n_sel;
+    const int en = in ? a.by_R.div(row) : 0, r = in ? row - en * a.R : 0;
+    const int e = in ? entry[en] : 0;
+    const int h = grp * a.R + r, t = a.q0 + a.by_sel.div(e);
+    me.keys = in ? max(0, min(KT, pos0 + t - k0 + 1)) : 0;
+    me.place = (((size_t)bg * a.nq * a.n_sel + e) * a.R + r) * per + sub;
+    const size_t at = ((size_t)b * a.H + h) * a.Tq + t;
+    const float x = in ? lse[at] : -INFINITY;
+    me.l2 = x == -INFINITY ? INFINITY : x * kLog2e;
+    me.dl = in ? w.delta[at] : 0.f;
     const unsigned long long sq = reinterpret_cast<unsigned long long>(q + row_off(a.sq, b, h, t));
     const unsigned long long so = reinterpret_cast<unsigned long long>(d_o + row_off(sdo, b, h, t));
+#pragma unroll
     for (int i = lane; i < 16 * (D / 8); i += 32) {
-      const int r = i / (D / 8), c = (i % (D / 8)) * 8;
-      const __nv_bfloat16* pq = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, sq, r));
-      const __nv_bfloat16* po = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, so, r));
-      const bool ok = __shfl_sync(0xffffffffu, int(in), r) != 0;
-      cp_async16(smem_u32(dq_ + r * L::LD + c), pq + c, ok);
-      cp_async16(smem_u32(dq_ + L::RW + r * L::LD + c), po + c, ok);
+      const int rr = i / (D / 8), c = (i % (D / 8)) * 8;
+      const __nv_bfloat16* pq = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, sq, rr));
+      const __nv_bfloat16* po = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, so, rr));
+      const bool ok = base + 16 * wp + rr < r1;
+      cp_async16(smem_u32(dq_ + rr * L::LD + c), pq + c, ok);
+      cp_async16(smem_u32(dq_ + L::RW + rr * L::LD + c), po + c, ok);
     }
   };
-  fetch(r0, 0);
+  Row me, next = {0, 0, INFINITY, 0.f};
+  fetch(r0, 0, me);
   cp_async_commit();
   cp_async_wait<0>();
   __syncthreads();
@@ -113,25 +125,14 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
 #pragma unroll
     for (int i = 0; i < 4; ++i) gk[n][i] = gv[n][i] = 0.f;
 
-  for (int base = r0, st = 0; base < r1; base += kGradTile, st ^= L::ST - 1) {
-    if (L::ST == 2 && base + kGradTile < r1) fetch(base + kGradTile, st ^ 1);
+  for (int base = r0, st = 0; base < r1; base += kGradTile, st ^= L::ST - 1, me = next) {
+    if (L::ST == 2 && base + kGradTile < r1) fetch(base + kGradTile, st ^ 1, next);
     cp_async_commit();
     const int ra = base + 16 * wp + g, rb = ra + 8;
-    int na = 0, nb = 0;  // keys of this tile the two rows see
-    size_t oa = 0, ob = 0;
-    float la = INFINITY, lb = INFINITY, da = 0.f, db = 0.f;
-    auto row = [&](int r, int& n, size_t& o, float& l2, float& dl) {
-      if (r >= r1) return;
-      const int e = entry[r / a.R], t = a.q0 + e / a.n_sel;
-      n = max(0, min(KT, pos0 + t - k0 + 1));
-      o = (((size_t)bg * a.nq * a.n_sel + e) * a.R + r % a.R) * per + sub;
-      const size_t at = ((size_t)b * a.H + grp * a.R + r % a.R) * a.Tq + t;
-      const float x = lse[at];
-      l2 = x == -INFINITY ? INFINITY : x * kLog2e;
-      dl = w.delta[at];
-    };
-    row(ra, na, oa, la, da);
-    row(rb, nb, ob, lb, db);
+    const int na = __shfl_sync(0xffffffffu, me.keys, g), nb = __shfl_sync(0xffffffffu, me.keys, g + 8);
+    const float la = __shfl_sync(0xffffffffu, me.l2, g), lb = __shfl_sync(0xffffffffu, me.l2, g + 8);
+    const float da = __shfl_sync(0xffffffffu, me.dl, g), db = __shfl_sync(0xffffffffu, me.dl, g + 8);
+    const bool masked = __any_sync(0xffffffffu, me.keys < KT);  // rows of the block's own queries, or none
     if (L::ST == 2) cp_async_wait<1>(); else cp_async_wait<0>();
     __syncwarp();
     const __nv_bfloat16* Qs = Rs + st * 2 * L::RW;
@@ -165,10 +166,12 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int col = 8 * n + 2 * qd + i;
-          p[i] = col < na ? exp2f(fmaf(sc[n][i], c2, -la)) : 0.f;
-          p[2 + i] = col < nb ? exp2f(fmaf(sc[n][2 + i], c2, -lb)) : 0.f;
-          s[i] = col < na ? p[i] * (dp[n][i] - da) * a.scale : 0.f;
-          s[2 + i] = col < nb ? p[2 + i] * (dp[n][2 + i] - db) * a.scale : 0.f;
+          p[i] = ex2(fmaf(sc[n][i], c2, -la));
+          p[2 + i] = ex2(fmaf(sc[n][2 + i], c2, -lb));
+          s[i] = p[i] * ((dp[n][i] - da) * a.scale);
+          s[2 + i] = p[2 + i] * ((dp[n][2 + i] - db) * a.scale);
+          if (masked && col >= na) p[i] = s[i] = 0.f;
+          if (masked && col >= nb) p[2 + i] = s[2 + i] = 0.f;
         }
         const int at = (16 * wp + g) * L::LP + 8 * n + 2 * qd;
         const uint32_t s0 = pack_bf16(s[0], s[1]), s1 = pack_bf16(s[2], s[3]);
@@ -238,13 +241,20 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     }
     float xa = 0.f, xb = 0.f;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int n = 0; n < D / 8; ++n) {
+      xa = fmaxf(xa, fmaxf(fabsf(acc[n][0]), fabsf(acc[n][1])));
+      xb = fmaxf(xb, fmaxf(fabsf(acc[n][2]), fabsf(acc[n][3])));
+    }
+    if (__any_sync(0xffffffffu, xa == INFINITY || xb == INFINITY)) {  // the largest finite one
+      xa = xb = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float u = fabsf(acc[n][i]), z = fabsf(acc[n][2 + i]);
-        if (u < INFINITY) xa = fmaxf(xa, u);
-        if (z < INFINITY) xb = fmaxf(xb, z);
-      }
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (fabsf(acc[n][i]) < INFINITY) xa = fmaxf(xa, fabsf(acc[n][i]));
+          if (fabsf(acc[n][2 + i]) < INFINITY) xb = fmaxf(xb, fabsf(acc[n][2 + i]));
+        }
+    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, o));
@@ -253,6 +263,7 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     xa = fmaxf(xa, 2.3509887e-38f);  // 2^-125: its reciprocal is still finite
     xb = fmaxf(xb, 2.3509887e-38f);
     const float va = 1.f / xa, vb = 1.f / xb;
+    const size_t oa = __shfl_sync(0xffffffffu, me.place, g), ob = __shfl_sync(0xffffffffu, me.place, g + 8);
     if (qd == 0) {
       if (ra < r1) w.mul[oa] = xa;
       if (rb < r1) w.mul[ob] = xb;
@@ -268,15 +279,15 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     }
     __syncwarp();
     __half* part = static_cast<__half*>(w.part);
+#pragma unroll
     for (int i = lane; i < 16 * (D / 8); i += 32) {
       const int r = i / (D / 8), c = (i % (D / 8)) * 8;
-      const size_t ua = __shfl_sync(0xffffffffu, oa, (r & 7) * 4), ub = __shfl_sync(0xffffffffu, ob, (r & 7) * 4);
+      const size_t u = __shfl_sync(0xffffffffu, me.place, r);
       if (base + 16 * wp + r < r1)
-        *reinterpret_cast<uint4*>(part + (r < 8 ? ua : ub) * D + c) =
-            *reinterpret_cast<const uint4*>(stage + r * L::LD + c);
+        *reinterpret_cast<uint4*>(part + u * D + c) = *reinterpret_cast<const uint4*>(stage + r * L::LD + c);
     }
     __syncwarp();  // before the next fetch into these rows
-    if (L::ST == 1 && base + kGradTile < r1) fetch(base + kGradTile, 0);
+    if (L::ST == 1 && base + kGradTile < r1) fetch(base + kGradTile, 0, next);
   }
   cp_async_wait<0>();
   float* kp = w.kv + (size_t)blockIdx.x * 2 * KT * D;
@@ -313,38 +324,55 @@ k_blk_delta(BlkArgs a, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16*
   if (in && c == 0) delta[i] = s;
 }
 
-// A row of dq from its parts, in list order; pairs without keys have none.
+// A row of dq from its parts, in list order; pairs without keys have none.  As in the
+// forward's join a lane looks up every LN-th part, and 4 rows' loads are in flight.
 template <int D>
 __global__ void __launch_bounds__(256)
 k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ dq,
          sdm_strides sdq, int kt) {
   constexpr int LN = D / 8;
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
-  const int c = (threadIdx.x % LN) * 8;
-  if (i >= (long long)a.B * a.G * a.nq * a.R) return;
-  const int r = int(i % a.R), per = a.bs / kt;
-  const long long bt = i / a.R;
-  const int t = int(bt % a.nq), bg = int(bt / a.nq), b = bg / a.G, h = (bg - b * a.G) * a.R + r;
+  const int ln = threadIdx.x % LN, c = ln * 8;
+  const bool in = i < (long long)a.B * a.G * a.nq * a.R;
+  const long long i0 = in ? i : 0, bt = i0 / a.R;
+  const int r = int(i0 - bt * a.R), per = a.bs / kt;  // per: 1 or 2 parts a pair
+  const int bg = int(bt / a.nq), t = int(bt - (long long)bg * a.nq), b = bg / a.G, h = (bg - b * a.G) * a.R + r;
   const int32_t* list = idx + ((size_t)bg * a.Tq + a.q0 + t) * a.n_sel;
-  const int p = blk_pos0(a, b) + a.q0 + t;
+  const int p = blk_pos0(a, b) + a.q0 + t, parts = a.n_sel * per;
+  // part y: slot y / per, keys (y % per) kt .. of its block
+  auto place = [&](int y) {
+    const int s = per == 2 ? y >> 1 : y;
+    return (((size_t)bt * a.n_sel + s) * a.R + r) * per + (per == 2 ? y & 1 : 0);
+  };
   const __half* part = static_cast<const __half*>(w.part) + c;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.n_sel; ++s) {
-    const int n = blk_keys(a, list[s], p);
-    for (int u = 0; u * kt < n; ++u) {
-      const size_t at = (((size_t)bt * a.n_sel + s) * a.R + r) * per + u;
-      const float f = w.mul[at];
-      const uint4 x = *reinterpret_cast<const uint4*>(part + at * D);
-      const __half2* hx = reinterpret_cast<const __half2*>(&x);
+  for (int y0 = 0; y0 < parts; y0 += LN) {
+    const int y = y0 + ln;
+    float f = -1.f;  // no part
+    if (y < parts && blk_keys(a, list[per == 2 ? y >> 1 : y], p) > (per == 2 && (y & 1) ? kt : 0)) f = w.mul[place(y)];
+#pragma unroll
+    for (int z0 = 0; z0 < LN; z0 += 4) {
+      uint4 x[4];
+      float fz[4];
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
-        const float2 y = __half22float2(hx[z]);
-        acc[2 * z] = fmaf(f, y.x, acc[2 * z]);
-        acc[2 * z + 1] = fmaf(f, y.y, acc[2 * z + 1]);
+        fz[z] = __shfl_sync(0xffffffffu, f, z0 + z, LN);
+        x[z] = make_uint4(0u, 0u, 0u, 0u);
+        if (fz[z] != -1.f) x[z] = *reinterpret_cast<const uint4*>(part + place(y0 + z0 + z) * D);
+      }
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const __half2* hx = reinterpret_cast<const __half2*>(&x[z]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 v = __half22float2(hx[u]);
+          acc[2 * u] = fmaf(fz[z], v.x, acc[2 * u]);
+          acc[2 * u + 1] = fmaf(fz[z], v.y, acc[2 * u + 1]);
+        }
       }
     }
   }
-  Vec<__nv_bfloat16, 8>::store(dq + row_off(sdq, b, h, a.q0 + t) + c, acc);
+  if (in) Vec<__nv_bfloat16, 8>::store(dq + row_off(sdq, b, h, a.q0 + t) + c, acc);
 }
 
 // dk, dv of 4 columns of a key: the items of its block in order.  With several passes

@@ -75,9 +75,9 @@ static cudaError_t launch_carry(const Carry& c0, const Carry& c1, int both, cons
   return cudaGetLastError();
 }
 
-cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, int BH, int nseg, int PN,
-                             cudaStream_t s) {
-  const Carry c = {segS, S0, nullptr, 0};
+cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, float* S_end, int BH,
+                             int nseg, int PN, cudaStream_t s) {
+  const Carry c = {segS, S0, S_end, 0};
   return launch_carry(c, c, 0, segG, BH, nseg, PN, s);
 }
 
@@ -377,7 +377,7 @@ static cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, const void* x, const fl
     k_ssm_walk<Tin, false><<<grid, kWalkThreads, smem, s>>>(
         a, (const Tin*)x, dt, A, (const Tin*)Bm, (const Tin*)Cm, D, S, lengths, (Tin*)y, segS, segG);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_ssm_carry(segS, segG, S, a.B * a.H, a.nseg, a.P * a.N, s)) !=
+    if ((e = launch_ssm_carry(segS, segG, S, nullptr, a.B * a.H, a.nseg, a.P * a.N, s)) !=
         cudaSuccess)
       return e;
   }

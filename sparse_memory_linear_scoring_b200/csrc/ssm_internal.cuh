@@ -68,8 +68,9 @@ __device__ __forceinline__ float decay_between(float hi_t, float lo_t, float hi_
 // Launchers.  The states kernel writes, per (head, segment), the segment's own
 // contribution to the state and its total log2 decay; the carry kernel turns the
 // former into the state before each segment.
-cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, int BH, int nseg, int PN,
-                             cudaStream_t s);
+// S_end (may be S0 itself, or NULL) gets the last state.
+cudaError_t launch_ssm_carry(float* segS, const float* segG, const float* S0, float* S_end, int BH,
+                             int nseg, int PN, cudaStream_t s);
 
 // The tensor-core walk takes bf16 inputs of widths 64 and 128 whose views allow
 // 16-byte pieces.

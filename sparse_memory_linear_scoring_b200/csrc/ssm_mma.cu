@@ -10,10 +10,12 @@
 //   product: one rounding of a weight, below that of y itself),
 //   y = M x + exp(g_t) (C S^T) + D x   (S rounded to bf16 for this product only),
 //   S = exp(g_Q) S + (w x)^T B with w_j = exp(g_Q - g_j) dt_j.
-// S itself is an output in float32 and is carried over thousands of steps, so w x is
-// split into three bf16 parts (what is left is below 2^-24) against the exact B:
-// three times the products of that term, which a bf16 or even a two-part (2^-16)
-// operand would make 400 or 2 times less exact than float32 sums.
+// S itself is an output in float32 and is carried over thousands of steps, so where it
+// becomes one (a segment's own contribution; a walk of one segment) w x is split into
+// three bf16 parts (what is left is below 2^-24) against the exact B.  In the second walk
+// of several segments S only makes y, whose product takes it rounded to bf16: there two
+// parts do (2^-16 of a term beside 2^-9), a fifth fewer products at 128 x 128.  The last
+// state then comes from the carry.
 #include "mma_dev.cuh"
 #include "ssm_internal.cuh"
 
@@ -51,7 +53,7 @@ __device__ __forceinline__ void tile_decay(float* dec, float d0, float d1, float
   }
 }
 
-template <int P, int N, bool OUT>
+template <int P, int N, bool OUT, int PARTS>
 __global__ void __launch_bounds__(P * 2)
 k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restrict__ dt,
            const float* __restrict__ A, const __nv_bfloat16* __restrict__ Bm,
@@ -71,8 +73,6 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
   const int T = seq_len(lengths, b, a.T);
   const float Ah = A[h], Dh = OUT && D ? D[h] : 0.f;
   const int c0 = seg * a.cps, c1 = min(c0 + a.cps, a.nch);
-  // the state contribution of the last segment has no reader
-  if (!OUT && seg == a.nseg - 1) return;
 
   auto load = [&](int c) {
     __nv_bfloat16* s = st + (c & 1) * L::STAGE;
@@ -228,8 +228,8 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
     const float gq = hi[kTQ - 1] + lo[kTQ - 1];
     tot += gq;
     if (live > 0) {
-      // (w x)^T as A fragments in three parts, all 64 steps
-      uint32_t xw[4][3][4];
+      // (w x)^T as A fragments in parts, all 64 steps
+      uint32_t xw[4][PARTS][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t xf[4];
@@ -237,9 +237,10 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 w = *reinterpret_cast<const float2*>(wj + 16 * k + (i >> 1) * 8 + 2 * q);
-          uint32_t u[3];
-          split_bf16<3>(bf16_lo(xf[i]) * w.x, bf16_hi(xf[i]) * w.y, u);
-          xw[k][0][i] = u[0]; xw[k][1][i] = u[1]; xw[k][2][i] = u[2];
+          uint32_t u[PARTS];
+          split_bf16<PARTS>(bf16_lo(xf[i]) * w.x, bf16_hi(xf[i]) * w.y, u);
+#pragma unroll
+          for (int z = 0; z < PARTS; ++z) xw[k][z][i] = u[z];
         }
       }
       const float eq = exp2f(gq);
@@ -251,7 +252,7 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
           uint32_t bf[4];
           ldsm4t(bf, ab + 2 * frag_bt(lane, 16 * n, 16 * k, L::LN));
 #pragma unroll
-          for (int i = 2; i >= 0; --i) {  // small parts first
+          for (int i = PARTS - 1; i >= 0; --i) {  // small parts first
             mma_bf16(d0, xw[k][i], bf[0], bf[1]);
             mma_bf16(d1, xw[k][i], bf[2], bf[3]);
           }
@@ -271,7 +272,7 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
   }
   cp_async_wait<0>();
   float* out = OUT ? S + size_t(bh) * PN : slot;
-  if (!OUT || seg == a.nseg - 1) {
+  if (!OUT || a.nseg == 1) {
 #pragma unroll
     for (int n = 0; n < N / 8; ++n) {
       float* p0 = out + (16 * wp + g) * N + 8 * n + 2 * q;
@@ -289,23 +290,18 @@ static cudaError_t launch_tile(const SsmArgs& a, const void* x, const float* dt,
                                cudaStream_t s) {
   using bf = __nv_bfloat16;
   const unsigned grid = unsigned(a.B * a.H) * unsigned(a.nseg);
-  cudaError_t e;
-  if (a.nseg > 1) {
-    const int sm = int(SsmTile<P, N, false>::smem);
-    if ((e = cudaFuncSetAttribute(k_ssm_tile<P, N, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)) != cudaSuccess)
-      return e;
-    k_ssm_tile<P, N, false><<<grid, P * 2, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm,
-                                                   D, S, lengths, (bf*)y, segS, segG);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_ssm_carry(segS, segG, S, a.B * a.H, a.nseg, P * N, s)) != cudaSuccess)
-      return e;
-  }
-  const int sm = int(SsmTile<P, N, true>::smem);
-  if ((e = cudaFuncSetAttribute(k_ssm_tile<P, N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)) != cudaSuccess)
-    return e;
-  k_ssm_tile<P, N, true><<<grid, P * 2, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm, D,
-                                                S, lengths, (bf*)y, segS, segG);
-  return cudaGetLastError();
+  const int s0 = int(SsmTile<P, N, false>::smem), s1 = int(SsmTile<P, N, true>::smem);
+  auto go = [&](auto kernel, int sm) -> cudaError_t {
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    if (r != cudaSuccess) return r;
+    kernel<<<grid, P * 2, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm, D, S, lengths,
+                                   (bf*)y, segS, segG);
+    return cudaGetLastError();
+  };
+  if (a.nseg == 1) return go(k_ssm_tile<P, N, true, 3>, s1);
+  cudaError_t e = go(k_ssm_tile<P, N, false, 3>, s0);
+  if (e == cudaSuccess) e = launch_ssm_carry(segS, segG, S, S, a.B * a.H, a.nseg, P * N, s);
+  return e == cudaSuccess ? go(k_ssm_tile<P, N, true, 2>, s1) : e;
 }
 
 cudaError_t launch_ssm_fwd_mma(const SsmArgs& a, const void* x, const float* dt, const float* A,
