@@ -382,9 +382,10 @@ extern "C" int sdm_block_forward(const void* q, const void* k, const void* v, co
   if (!aligned_to(workspace, 16)) return SDM_ERR_ALIGN;
   const BlkArgs a = blk_args(dims, views, lengths);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool tiles = blk_tiles_pay(dims) && view_aligned(q, a.sq, 2, 16) && view_aligned(k, a.sk, 2, 16) &&
-                     view_aligned(v, a.sv, 2, 16) && view_aligned(o, a.so, 2, 16);
-  const cudaError_t e = tiles ? launch_blk_fwd_mma(dims, a, q, k, v, idx, o, lse, workspace, s)
-                              : launch_blk_row_fwd(a, dims->in_dtype == SDM_DTYPE_BF16, q, k, v, idx, o, lse, s);
+  const bool pieces = dims->in_dtype == SDM_DTYPE_BF16 && view_aligned(q, a.sq, 2, 16) &&
+                      view_aligned(k, a.sk, 2, 16) && view_aligned(v, a.sv, 2, 16) && view_aligned(o, a.so, 2, 16);
+  const cudaError_t e = !pieces ? launch_blk_row_fwd(a, dims->in_dtype == SDM_DTYPE_BF16, q, k, v, idx, o, lse, s)
+                        : blk_tiles_pay(dims) ? launch_blk_fwd_mma(dims, a, q, k, v, idx, o, lse, workspace, s)
+                                              : launch_blk_step(a, q, k, v, idx, o, lse, s);
   return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }

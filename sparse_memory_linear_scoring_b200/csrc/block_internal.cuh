@@ -1,5 +1,6 @@
 // block_internal.cuh -- sparse attention over selected blocks (block_select.cu,
-// block_attn.cu, block_bwd.cu, block_mma.cu, block_bwd_mma.cu): sizes, the plan, shared device code.
+// block_attn.cu, block_bwd.cu, block_mma.cu, block_bwd_mma.cu,
+// block_step.cu): sizes, the plan, shared device code.
 //
 // Keys are cut into blocks of `block` consecutive positions.  The query at
 // position p (the last Tq of the sequence's keys) has a list of blocks; it
@@ -94,6 +95,10 @@ bool blk_tiles_pay(const sdm_block_dims* d);   // whether the tensor-core pass i
 cudaError_t launch_blk_fwd_mma(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,
                                const void* v, const int32_t* idx, void* o, float* lse,
                                void* workspace, cudaStream_t s);
+
+// Query by query on the tensor cores (block_step.cu); bf16, views in 16-byte pieces.
+cudaError_t launch_blk_step(const BlkArgs& a, const void* q, const void* k, const void* v,
+                            const int32_t* idx, void* o, float* lse, cudaStream_t s);
 
 // Tensor-core backward pass (block_bwd_mma.cu).
 struct BlkBwdWs {
