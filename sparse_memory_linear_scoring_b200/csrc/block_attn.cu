@@ -1,6 +1,6 @@
 // block_attn.cu -- attention over listed blocks, query by query on CUDA cores: single
-// tokens, short calls and float32 inputs, forward and the query's gradient; and the
-// C ABI of the forward pass.
+// tokens and short calls whose views block_step.cu does not take, float32 inputs,
+// forward and the query's gradient; and the C ABI of the forward pass.
 //
 //   s_k = scale q.k over the listed keys at positions <= p;  o = sum softmax(s)_k v_k;
 //   lse = log sum exp(s_k);  no key: o = 0, lse = -inf.
@@ -16,7 +16,6 @@
 // (l % LN) * (32 / LN) + l / LN.  The warps of up to 8 CTAs of a cluster share a
 // query's list, so that a few queries fill the card, and join their running maxima,
 // sums and rows through distributed shared memory: one launch, no workspace.
-// 64 sequences of up to 4096 keys, 16 heads of 64 on 4: see k_blk_row's launcher.
 #include <cooperative_groups.h>
 
 #include "block_internal.cuh"
@@ -289,8 +288,10 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
   if (cs > 1) cl.sync();  // the others may still be reading this CTA's rows
 }
 
-// CTAs that share a query: 1 while the queries alone are 4 CTAs an SM, more while a
-// warp would still have at least one piece of 32 keys.
+// CTAs that share a query: more than one while they all fit the card at 4 an SM and a
+// warp has a piece of 32 keys.  float32, 16 blocks of 64, d = 64, 4 groups of 4 heads,
+// clusters of 1 / 2 / 4 / 8: 1 sequence 26 / 16 / 10 / 8 us, 32 sequences
+// 29 / 20 / 16 / 22, 64 sequences 41 / 30 / 35 / 46.
 template <typename Tin, int D, int RH, bool BWD>
 static cudaError_t launch_row(const BlkArgs& a, const void* q, const void* k, const void* v,
                               const int32_t* idx, void* o, float* lse, const void* d_o,
@@ -299,7 +300,7 @@ static cudaError_t launch_row(const BlkArgs& a, const void* q, const void* k, co
   const int es = int(sizeof(Tin)), hc = (a.R + RH - 1) / RH, pieces = a.n_sel * (a.bs / 32);
   const long long items = (long long)a.B * a.G * a.Tq * hc;
   int cs = 1;
-  while (cs < kRowCluster && items * cs < 4 * 148 && 2 * cs * kRowWarps <= pieces) cs *= 2;
+  while (cs < kRowCluster && 2 * items * cs <= 4 * 148 && 2 * cs * kRowWarps <= pieces) cs *= 2;
   if (items * cs >= (1LL << 31)) return cudaErrorInvalidConfiguration;
   int vec = view_aligned(q, a.sq, es, 16) ? 1 : 0;
   if (BWD && view_aligned(d_o, sdo, es, 16) && view_aligned(o, a.so, es, 16)) vec |= 2;

@@ -147,7 +147,7 @@ static size_t blk_delta_bytes(const sdm_block_dims* d) {
 extern "C" size_t sdm_block_backward_workspace_bytes(const sdm_block_dims* dims) {
   if (blk_check(dims) != SDM_OK) return 0;
   size_t n = blk_delta_bytes(dims) + blk_plan(dims, dims->Tq, 512, nullptr).bytes;
-  if (blk_tiles_pay(dims)) {  // views that are not aligned still take the other path
+  if (blk_bwd_tiles_pay(dims)) {  // views that are not aligned still take the other path
     const size_t t = blk_bwd_ws(dims, blk_bwd_chunk(dims), nullptr).bytes;
     if (t > n) n = t;
   }
@@ -174,7 +174,7 @@ extern "C" int sdm_block_backward(const void* q, const void* k, const void* v, c
   const BlkArgs a = blk_args(dims, views, lengths);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const sdm_block_views* gv = grad_views;
-  if (blk_tiles_pay(dims) && view_aligned(q, a.sq, 2, 16) && view_aligned(k, a.sk, 2, 16) &&
+  if (blk_bwd_tiles_pay(dims) && view_aligned(q, a.sq, 2, 16) && view_aligned(k, a.sk, 2, 16) &&
       view_aligned(v, a.sv, 2, 16) && view_aligned(o, a.so, 2, 16) && view_aligned(d_o, gv->o, 2, 16) &&
       view_aligned(dq, gv->q, 2, 16) && view_aligned(dk, gv->k, 2, 16) && view_aligned(dv, gv->v, 2, 16))
     return launch_blk_bwd_mma(dims, a, q, k, v, idx, o, lse, d_o, dq, dk, dv, gv, workspace, s) == cudaSuccess

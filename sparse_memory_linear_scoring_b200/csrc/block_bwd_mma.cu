@@ -414,6 +414,10 @@ k_blk_dkv(BlkArgs a, BlkBwdWs w, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* 
 // ---------------------------------------------------------------- host side
 static int grad_keys(const sdm_block_dims* d) { return d->block < 64 ? 32 : 64; }
 
+// Fewer queries than half a tile leave it mostly empty, and the query-by-query kernels
+// have none of the plan's launches.
+bool blk_bwd_tiles_pay(const sdm_block_dims* d) { return d->in_dtype == SDM_DTYPE_BF16 && d->Tq >= 32; }
+
 // Queries per pass: as many as keep the parts of dq within 2 GiB (at least 128).
 int blk_bwd_chunk(const sdm_block_dims* d) {
   const long long per = (long long)d->B * d->H * d->n_sel * (d->block / grad_keys(d)) * (d->d * 2 + 4);

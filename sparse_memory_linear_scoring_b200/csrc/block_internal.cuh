@@ -111,6 +111,7 @@ struct BlkBwdWs {
   size_t bytes;
 };
 BlkBwdWs blk_bwd_ws(const sdm_block_dims* d, int nq, void* base);
+bool blk_bwd_tiles_pay(const sdm_block_dims* d);
 int blk_bwd_chunk(const sdm_block_dims* d);
 cudaError_t launch_blk_bwd_mma(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,
                                const void* v, const int32_t* idx, const void* o, const float* lse,

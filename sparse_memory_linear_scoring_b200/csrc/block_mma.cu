@@ -346,8 +346,15 @@ k_blk_join(BlkArgs a, BlkFwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16
 }
 
 // ---------------------------------------------------------------- host side
+// Query by query the listed keys and values are read anew for each query (and 16 heads),
+// at about 4 TB/s; block by block the plan, the tiles and the join take about 33 us
+// before the work counts, and short calls have few queries a block anyway.  d = 128,
+// 16 blocks of 64, one sequence, 4 groups: 64 queries (134 MB) 33 us query by query, 39
+// block by block; 128 queries 64 and 44; 16 groups, 32 queries 64 and 56.
 bool blk_tiles_pay(const sdm_block_dims* d) {
-  return d->in_dtype == SDM_DTYPE_BF16 && d->Tq >= 32;
+  const long long hc = (d->H / d->G + 15) / 16;
+  return d->in_dtype == SDM_DTYPE_BF16 && d->Tq >= 32 &&
+         hc * d->B * d->G * d->Tq * d->n_sel * d->block * d->d * 4 > (128LL << 20);
 }
 
 // Queries per pass: as many as keep the partials within 2 GiB (at least 128).

@@ -188,17 +188,26 @@ k_blk_select(BlkArgs a, sdm_strides skc, const Tin* __restrict__ q, const Tin* _
 #pragma unroll
       for (int n = 0; n < 4; ++n)  // columns behind the last block repeat it and are not read back
         kp[n] = kc + row_off(skc, b, g, min(j0 + jt + 8 * n + gr, nj - 1)) + 4 * qd;
-      for (int k = 0; k < d; k += 16) {
-        float f[4][4];
+      float nx[4][4];  // the next 16 columns are on their way while these are multiplied
+      auto fetch = [&](int k) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           if (vec & 2) {
-            Vec<Tin, 4>::load(kp[n] + k, f[n]);
+            Vec<Tin, 4>::load(kp[n] + k, nx[n]);
           } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) f[n][u] = to_f32(kp[n][k + u]);
+            for (int u = 0; u < 4; ++u) nx[n][u] = to_f32(kp[n][k + u]);
           }
         }
+      };
+      fetch(0);
+      for (int k = 0; k < d; k += 16) {
+        float f[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) f[n][u] = nx[n][u];
+        if (k + 16 < d) fetch(k + 16);
         double af[8];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {

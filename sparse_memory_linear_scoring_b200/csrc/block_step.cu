@@ -10,7 +10,8 @@
 // one launch without a workspace fills the card from few sequences.
 // block_attn.cu has the formulas, and the CUDA-core kernel for views that cannot be read
 // in 16-byte pieces; per head and key that one needs about 100 instructions where a tile
-// needs 200 a piece in all (64 sequences of up to 4096 keys, 16 heads of 64 on 4: 35 us).
+// needs 200 a piece in all (64 sequences of up to 4096 keys, 16 heads of 64 on 4: 35 us
+// there, 14 here, 4.8 TB/s).
 #include <cooperative_groups.h>
 
 #include "block_internal.cuh"
@@ -216,8 +217,11 @@ k_blk_step(BlkArgs a, const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* 
   if (cs > 1) cl.sync();  // the others may still be reading this CTA's rows
 }
 
-// CTAs that share a query: 1 while the queries alone are 4 CTAs an SM, more while a
-// warp would still have at least one piece.
+// CTAs that share a query: more than one only while they all fit the card at one an SM
+// and a warp has two pieces, since launching and joining a cluster costs more than it
+// saves elsewhere.  16 blocks of 64, d = 64, 4 groups, clusters of 1 / 2 / 4 / 8:
+// 1 sequence 10.3 / 8.0 / 6.7 / 6.9 us, 16 sequences 10.5 / 8.3 / 8.8 / 16.3,
+// 64 sequences 14.0 / 20.5 / 25.7 / 47.2; 4 sequences with 64 blocks 33 / 20 / 13 / 11.
 template <int D>
 static cudaError_t launch_step(const BlkArgs& a, const void* q, const void* k, const void* v,
                                const int32_t* idx, void* o, float* lse, cudaStream_t s) {
@@ -225,7 +229,7 @@ static cudaError_t launch_step(const BlkArgs& a, const void* q, const void* k, c
   const int hc = (a.R + 15) / 16, pieces = a.n_sel * (a.bs / kPiece);
   const long long items = (long long)a.B * a.G * a.Tq * hc;
   int cs = 1;
-  while (cs < kStepCluster && items * cs < 4 * 148 && 2 * cs * kStepWarps <= pieces) cs *= 2;
+  while (cs < kStepCluster && 2 * items * cs <= 148 && 4 * cs * kStepWarps <= pieces) cs *= 2;
   if (items * cs >= (1LL << 31)) return cudaErrorInvalidConfiguration;
   const int sm = int(StepTile<D>::smem);
   cudaError_t e = cudaFuncSetAttribute(k_blk_step<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
