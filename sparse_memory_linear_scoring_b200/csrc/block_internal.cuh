@@ -90,6 +90,8 @@ struct BlkFwdWs {
   size_t bytes;
 };
 BlkFwdWs blk_fwd_ws(const sdm_block_dims* d, int nq, void* base);
+cudaError_t launch_blk_tc(const BlkArgs& a, const BlkFwdWs& w, unsigned grid, const void* q, const void* k,
+                          const void* v, cudaStream_t s);  // the tiles (block_tc.cu)
 int blk_chunk(const sdm_block_dims* d);        // queries per pass
 bool blk_tiles_pay(const sdm_block_dims* d);   // whether the tensor-core pass is taken
 cudaError_t launch_blk_fwd_mma(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,

@@ -238,6 +238,45 @@ def test_small_values(dtype):
     R.close(o, ref["o"], _k(dtype, 64, ref) * ref["o_mag"], "o")
 
 
+@pytest.mark.parametrize("Tq", [1, 150, 700])
+def test_scale_zero(Tq):
+    """Equal weights over the listed keys."""
+    q, k, v, g = _make(2, 16, 4, Tq, 700, 128, BF)
+    idx = R.select(q, R.pool(k, 64), 9, 64, 700)
+    _check_forward(q, k, v, idx, 64, BF, scale=0.0)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("block", [32, 64, 128])
+def test_tiles(d, block):
+    """Enough listed keys for the block-by-block kernels at every width and block, items
+    of several row tiles, blocks that some queries see in part, long and short rows."""
+    q, k, v, g = _make(2, 12, 2, 1500, 1777, d, BF, "token")
+    n = torch.tensor([1777, 1201], dtype=torch.int32, device="cuda")
+    idx = R.select(q, R.pool(k, block), 24, block, 1777, n)
+    v[0, 0, 800], v[0, 0, 1000, 3], v[1, 1, 7, 1] = float("inf"), float("nan"), float("-inf")
+    ref = R.block_attention(q, k, v, idx, block, 0.3, n)
+    o, lse = sdm.block_forward(q, k, v, idx, block=block, scale=0.3, lengths=n, return_lse=True)
+    # float64 products spread a NaN or infinity to every query of the group: compare the
+    # groups without one, and the others where their lists leave those keys out
+    for b, h0 in ((0, 6), (1, 0)):
+        one = {x: ref[x][b:b + 1, h0:h0 + 6] for x in ("o", "o_mag", "smag")}
+        R.close(o[b:b + 1, h0:h0 + 6], one["o"], _k(BF, d, one) * one["o_mag"], "o %d" % b)
+    clean = v.clone()
+    clean[0, 0, 800] = clean[0, 0, 1000, 3] = clean[1, 1, 7, 1] = 0
+    ref = R.block_attention(q, k, clean, idx, block, 0.3, n)
+    R.close(lse, ref["lse"], 2 * d * R.ADD * ref["smag"] + 2.0 ** -18, "lse")
+    pos = R.positions(2, 1500, 1777, n, q.device)
+    c = R.counts(idx, block, 1777, pos)
+    out = torch.where((c[0, 0, :, 800] + c[0, 0, :, 1000] > 0)[None, :, None], ref["o"][0, :6], o[0, :6].double())
+    one = {x: ref[x][0, :6] for x in ("o", "o_mag", "smag")}
+    R.close(out.to(BF), one["o"], (_k(BF, d, one) + 2.0 ** -8) * one["o_mag"], "o of rows without such keys")
+    inf, nan = c[0, 0, :, 800] > 0, c[0, 0, :, 1000] > 0
+    got = o[0, :6]
+    assert (got[:, inf & ~nan] == math.inf).all() and got[:, nan, 3].isnan().all()
+    assert torch.equal(o[1, 6:, :, 1] == -math.inf, (c[1, 1, :, 7] > 0)[None].expand(6, -1))
+
+
 def test_many_passes():
     """Lists so long that queries are taken in passes, with repeated entries."""
     q, k, v, g = _make(8, 64, 4, 300, 300, 128, BF)
