@@ -1,6 +1,6 @@
 // block_bwd_mma.cu -- gradients of block-selected attention on the tensor cores (bf16).
 //
-// As in block_mma.cu a CTA takes one block of keys (64 at most) and up to kItemRows of
+// As in block_mma.cu a CTA takes one block of keys (64 at most) and up to kGradRows of
 // the rows (pair, head of the group) that list it, so that K and V stay in shared
 // memory and dK and dV in registers while the rows stream past, 64 at a time:
 //     P = exp(scale Q K^T - lse),  dS = P (dO V^T - delta) scale,

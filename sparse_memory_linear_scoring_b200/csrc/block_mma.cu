@@ -5,7 +5,7 @@
 // tile.  The other way round every tile is full: a CTA takes one block of keys and
 // the list of (query, slot) pairs that name it (the plan of block_select.cu), and its
 // rows are those pairs times the heads of the group.  Keys and values are read once
-// per item of kItemRows rows; a row has one block of scores, so its softmax needs no
+// per item of 512 to 1024 rows; a row has one block of scores, so its softmax needs no
 // running maximum.  What this costs is a partial result per (query, slot, head) --
 // d halves, a log-sum-exp and a scale, written here and read once by the join:
 //     o = sum_s exp(lse_s - lse) o_s,   lse = log sum_s exp(lse_s).
@@ -19,7 +19,17 @@
 
 namespace sdm {
 
-constexpr int kItemRows = 512;
+// Rows of an item.  Its keys' load and the CTA's start cost as much as a tile of 128 rows
+// and a half; longer items share that among more, shorter ones keep three CTAs an SM busy
+// to the end: as long as there are four rounds of them, up to 1024 (8192 tokens, 16 heads
+// of 128: 445 us with 512, 422 with 1024, 434 with 2048).
+static int item_rows(const sdm_block_dims* d, int nq) {
+  const long long rows = (long long)d->B * d->H * nq * d->n_sel;
+  long long n = rows / (4 * 3 * 148);
+  n = n < 512 ? 512 : n > 1024 ? 1024 : n;
+  return int(n / 128 * 128);
+}
+
 // A row of o from its partials: D / 8 lanes a row.  A lane first takes every LN-th slot
 // of the list for the maximum and the sum, then each of LN slots at a time for its
 // weight, which the others get by shuffles, with 4 partial rows' loads in flight.  The
@@ -117,7 +127,7 @@ int blk_chunk(const sdm_block_dims* d) {
 
 BlkFwdWs blk_fwd_ws(const sdm_block_dims* d, int nq, void* base) {
   BlkFwdWs w;
-  w.plan = blk_plan(d, nq, kItemRows, base);
+  w.plan = blk_plan(d, nq, item_rows(d, nq), base);
   const size_t rows = size_t(d->B) * d->H * nq * d->n_sel;
   char* b = static_cast<char*>(base);
   size_t o = w.plan.bytes;

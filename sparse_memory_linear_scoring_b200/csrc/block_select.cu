@@ -156,6 +156,7 @@ k_blk_select(BlkArgs a, sdm_strides skc, const Tin* __restrict__ q, const Tin* _
     const int t = i / (d / 4), e = (i - t * (d / 4)) * 4;
     double s[4] = {0.0, 0.0, 0.0, 0.0};
     if (t < nq)
+#pragma unroll 4
       for (int r = 0; r < a.R; ++r) {
         const Tin* p = q + row_off(a.sq, b, g * a.R + r, q0 + t) + e;
         float f[4];

@@ -1,20 +1,22 @@
 // block_tc.cu -- the tiles of block-selected attention's forward pass on the
 // fifth-generation tensor cores (bf16).  block_mma.cu has the plan, the parts and the join.
 //
-// A CTA holds one block's keys and values and takes up to kItemRows of the rows (query
-// that lists the block, head of the group), 128 at a time, one row to a thread:
+// A CTA holds one block's keys and values and takes an item of the rows (query that
+// lists the block, head of the group), 128 at a time, one row to a thread:
 //   gather the rows' queries (cp.async into the 128-byte swizzle),
 //   S = Q K^T (tcgen05.mma, 128 x BS in TMEM),
 //   softmax of the thread's own row from TMEM, P as bf16 over the queries' place,
 //   O = P V (tcgen05.mma; V is MN-major as it lies, so nothing is transposed),
-//   O over the row's largest element as halves, a bulk copy per row.
-// The products take a few percent of the time; what bounds a tile is the softmax and
-// the conversion of O, about 900 instructions a thread (7 a row, where warp-level
-// fragments cost 65 a row: four lanes shared each row's maxima and sums, and every
-// operand went through registers), and the parts' bytes.  A tile is a chain of four
-// waits, so 3 CTAs an SM (at d = 128, by shared memory) run side by side instead of
-// one with more stages: the queries' place serves P and the outgoing rows, S and O
-// share TMEM columns.
+//   O over the row's largest element as halves, through shared memory to the parts.
+// The products take a few percent of the time.  What bounds a tile is the softmax, the
+// conversion of O, the gather and the way out, about 1600 instructions a thread (13 a
+// row and lane, where warp-level fragments cost 65: four lanes shared each row's maxima
+// and sums, and every operand went through registers), and a chain of four waits: 3 CTAs
+// an SM (at d = 128, by shared memory) run side by side instead of one with more stages,
+// so the queries' place serves P and the outgoing rows, and S and O share TMEM columns.
+// 8192 tokens, 2 sequences, 16 heads of 128 on 4, 16 blocks of 64: 422 us, of which the
+// 1.1 GB of parts take 100; two threads a row (24 warps an SM for 12) took 486, a bulk
+// copy for each outgoing row 444, paired float32 instructions 465 (register moves).
 #include <cuda_fp16.h>
 
 #include "block_internal.cuh"
@@ -110,14 +112,18 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
     cp_async16(aK + o, k + row_off(a.sk, b, grp, at) + 8 * c, in);
     cp_async16(aV + o, v + row_off(a.sv, b, grp, at) + 8 * c, in);
   }
-  // the thread's row of a tile: the keys it sees, its part's place, its query
-  int keys;
+  // the thread's row of a tile: the keys it sees, its part's place, its query.  peek sends
+  // for the row's list entry, look makes something of it when it has arrived.
+  int keys, en, ee = 0;
   size_t place;
   unsigned long long src;
+  auto peek = [&](int row) {
+    en = row < r1 ? a.by_R.div(row) : -1;
+    if (en >= 0) ee = entry[en];
+  };
   auto look = [&](int row) {
-    const bool in = row < r1;
-    const int en = in ? a.by_R.div(row) : 0, r = in ? row - en * a.R : 0;
-    const int e = in ? entry[en] : 0;
+    const bool in = en >= 0;
+    const int r = in ? row - en * a.R : 0, e = in ? ee : 0;
     const int t = a.q0 + a.by_sel.div(e);
     keys = in ? min(BS, pos0 + t - k0 + 1) : 0;
     place = ((size_t)bg * a.nq * a.n_sel + e) * a.R + r;
@@ -132,6 +138,7 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
     }
     cp_async_commit();
   };
+  peek(r0 + tid);
   look(r0 + tid);
   gather(r0);
   cp_async_wait<0>();
@@ -178,9 +185,7 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
                   sdesc(aK + (kk >> 2) * (BS * 128) + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
       umma_commit(&bars[0]);
     }
-    const int my_keys = keys;
-    const size_t my_place = place;
-    if (base + kTcRows < r1) look(base + kTcRows + tid);  // the next tile's rows, while S is made
+    if (base + kTcRows < r1) peek(base + kTcRows + tid);  // the next tile's rows
     mbar_wait(&bars[0], parity, gave_up);
     tc_fence_after();
     float l = 0.f, m = -INFINITY;
@@ -193,10 +198,10 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
 #pragma unroll
         for (int c = 0; c < BS; ++c) sc[c] = -sc[c];
       }
-      if (__any_sync(0xffffffffu, my_keys < BS)) {  // rows of the block's own queries, or none
+      if (__any_sync(0xffffffffu, keys < BS)) {  // rows of the block's own queries, or none
 #pragma unroll
         for (int c = 0; c < BS; ++c)
-          if (c >= my_keys) sc[c] = -INFINITY;
+          if (c >= keys) sc[c] = -INFINITY;
       }
 #pragma unroll
       for (int c = 0; c < BS; c += 2) m = fmaxf(m, fmaxf(sc[c], sc[c + 1]));
@@ -238,7 +243,7 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
         while (todo) {
           const int key = 32 * z + __ffs(todo) - 1;
           todo &= todo - 1;
-          if (key >= my_keys) continue;
+          if (key >= keys) continue;
           const float p = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
               work + swz(tid, key >> 3, kTcRows) + (key & 7) * 2));
           const __nv_bfloat16* vr = v + row_off(a.sv, b, grp, k0 + key);
@@ -282,14 +287,21 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
       // a wait that ran out poisons the row
       float2 ml = l == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(m + log2f(l), xm / l);
       if (*gave_up) ml = make_float2(NAN, NAN);
-      w.ml[my_place] = ml;
-      fence_async_smem();
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(part + my_place * D),
-                   "r"(smem_u32(orow)), "n"(2 * D) : "memory");
+      w.ml[place] = ml;
     }
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    __syncwarp();
+    // the warp's rows go out with consecutive lanes on consecutive pieces (a bulk copy a row
+    // took 2200 cycles a tile, 64 a copy)
+#pragma unroll
+    for (int i = lane; i < 32 * (D / 8); i += 32) {
+      const int rr = i / (D / 8), c = i % (D / 8);
+      const size_t to = __shfl_sync(0xffffffffu, place, rr);
+      if (base + 32 * wp + rr < r1)
+        *reinterpret_cast<uint4*>(part + to * D + 8 * c) =
+            *reinterpret_cast<const uint4*>(work + (32 * wp + rr) * L::OP + 16 * c);
+    }
     if (base + kTcRows < r1) {
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      look(base + kTcRows + tid);
       tc_fence_before();
       __syncthreads();  // the outgoing rows and O have been read
       gather(base + kTcRows);
@@ -299,7 +311,6 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
       tc_fence_after();
     }
   }
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (wp == 0) {

@@ -335,8 +335,8 @@ int ssm_check(const sdm_ssm_dims* d) {
 static void ssm_segments(const sdm_ssm_dims* d, int Q, SsmArgs* a) {
   a->Q = Q;
   a->nch = (d->T + Q - 1) / Q;
-  const long long BH = (long long)d->B * d->H;
-  long long nseg = (2 * 148 + BH - 1) / BH;
+  const long long BH = (long long)d->B * d->H * (Q == kSsmQT ? (d->d_v + 63) / 64 : 1);  // walks of a segment
+  long long nseg = 2 * 148 / BH;
   while (nseg > 1 && nseg * nseg > 64LL * a->nch) --nseg;
   if (nseg > a->nch) nseg = a->nch;
   if (nseg < 1) nseg = 1;

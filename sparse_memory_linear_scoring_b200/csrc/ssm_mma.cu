@@ -2,9 +2,12 @@
 // widths 64 and 128).  ssm_internal.cuh has the chunk formulas, ssm.cu the
 // segments.
 //
-// A CTA walks one segment of one head in chunks of 64 steps.  Warp w owns rows
-// 16 w .. 16 w + 15 of S, which stay in its registers as float32 accumulators from
-// chunk to chunk; the chunk's x, B and C tiles arrive by cp.async one chunk ahead.
+// A CTA walks one segment of 64 rows of one head's S in chunks of 64 steps (the rows of S
+// do not meet; at d_v = 128 the two halves share only the scores, a tenth of the
+// products, and two CTAs of 4 warps an SM, each at its own barriers, keep the tensor
+// cores busier than one of 8).  Warp w owns rows 16 w .. 16 w + 15, which stay in its
+// registers as float32 accumulators from chunk to chunk; the chunk's x, B and C tiles
+// arrive by cp.async one chunk ahead.
 // Per chunk:
 //   scores G = C B^T, weights M = mask exp(g_t - g_j) dt_j G (bf16 for the next
 //   product: one rounding of a weight, below that of y itself),
@@ -23,17 +26,15 @@ namespace sdm {
 
 constexpr int kTQ = kSsmQT;  // 64
 
-template <int P, int N, bool OUT>
+template <int N, bool OUT>
 struct SsmTile {
-  static constexpr int W = P / 16;                 // warps
+  static constexpr int P = 64;                     // rows of S
   static constexpr int LX = P + 8, LN = N + 8;     // pitches: ldmatrix without bank conflicts
   static constexpr int X = kTQ * LX, BC = kTQ * LN;
   static constexpr int STAGE = X + (OUT ? 2 : 1) * BC;   // bf16 elements
   static constexpr int SB = OUT ? P * LN : 0;            // S rounded to bf16
-  static constexpr int LY = 72;
-  static constexpr int YS = OUT ? W * 16 * LY : 0;       // y rows on their way out
   static constexpr int DEC = 5 * kTQ;                    // hi, lo, dt, exp(g), w
-  static constexpr size_t smem = size_t(2) * (2 * STAGE + SB + YS) + size_t(4) * 2 * DEC;
+  static constexpr size_t smem = size_t(2) * (2 * STAGE + SB) + size_t(4) * 2 * DEC;
 };
 
 // Warp 0: decays of one chunk from its steps 2 lane, 2 lane + 1.
@@ -53,23 +54,26 @@ __device__ __forceinline__ void tile_decay(float* dec, float d0, float d1, float
   }
 }
 
-template <int P, int N, bool OUT, int PARTS>
-__global__ void __launch_bounds__(P * 2)
+template <int N, bool OUT, int PARTS>
+__global__ void __launch_bounds__(128)
 k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restrict__ dt,
            const float* __restrict__ A, const __nv_bfloat16* __restrict__ Bm,
            const __nv_bfloat16* __restrict__ Cm, const float* __restrict__ D, float* __restrict__ S,
            const int32_t* __restrict__ lengths, __nv_bfloat16* __restrict__ y,
            float* __restrict__ segS, float* __restrict__ segG) {
-  using L = SsmTile<P, N, OUT>;
+  using L = SsmTile<N, OUT>;
+  constexpr int P = L::P;
   extern __shared__ __align__(16) unsigned char raw[];
   __nv_bfloat16* st = reinterpret_cast<__nv_bfloat16*>(raw);
   __nv_bfloat16* Sb = st + 2 * L::STAGE;
-  __nv_bfloat16* ys = Sb + L::SB;
-  float* dec = reinterpret_cast<float*>(ys + L::YS);
-  constexpr int NT = P * 2;
+  float* dec = reinterpret_cast<float*>(Sb + L::SB);
+  constexpr int NT = 128;
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
-  const int seg = blockIdx.x % a.nseg, bh = blockIdx.x / a.nseg;
+  const int seg = blockIdx.x % a.nseg, halves = a.P / P;
+  const int bp = blockIdx.x / a.nseg, bh = bp / halves, pr = (bp - bh * halves) * P;  // first row of S
   const int b = bh / a.H, h = bh - b * a.H, gr = h / a.hg;
+  x += pr;
+  y += pr;
   const int T = seq_len(lengths, b, a.T);
   const float Ah = A[h], Dh = OUT && D ? D[h] : 0.f;
   const int c0 = seg * a.cps, c1 = min(c0 + a.cps, a.nch);
@@ -99,8 +103,8 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
   // S rows 16 wp + g, + 8; columns 8 n + 2 q, + 1
   const int g = lane >> 2, q = lane & 3;
   float s[N / 8][4];
-  const size_t PN = size_t(P) * N;
-  float* slot = a.nseg > 1 ? segS + size_t(blockIdx.x) * PN : S + size_t(bh) * PN;
+  const size_t PN = size_t(a.P) * N;
+  float* slot = (a.nseg > 1 ? segS + (size_t(bh) * a.nseg + seg) * PN : S + size_t(bh) * PN) + size_t(pr) * N;
 #pragma unroll
   for (int n = 0; n < N / 8; ++n) {
     const float* p0 = slot + (16 * wp + g) * N + 8 * n + 2 * q;
@@ -131,6 +135,7 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
     cp_async_wait<1>();
     __syncthreads();  // chunk c's tiles, decays and bf16 state are in place
     const __nv_bfloat16* xs = st + (c & 1) * L::STAGE;
+    __nv_bfloat16* yw = st + (c & 1) * L::STAGE + L::X + L::BC + wp * 16 * L::LN;  // C rows of the warp
     const uint32_t ax = smem_u32(xs), ab = ax + 2 * L::X, ac = ab + 2 * L::BC;
     const float* dc = dec + (c & 1) * L::DEC;
     const float *hi = dc, *lo = dc + kTQ, *dts = dc + 2 * kTQ, *eg = dc + 3 * kTQ, *wj = dc + 4 * kTQ;
@@ -141,7 +146,7 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
     }
     const int t0 = c * kTQ, live = T - t0;
     if (OUT) {
-      const int rt = wp & 3, p0 = (wp >> 2) * 64;  // rows 16 rt.., columns p0 .. p0 + 63
+      const int rt = wp;  // rows 16 rt.. of y
       float acc[8][4];
       if (live > 16 * rt) {
         float sc[8][4];
@@ -162,7 +167,7 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
               mma_bf16(sc[2 * n + 1], af, bf[2], bf[3]);
             }
             uint32_t sf[4];
-            ldsm4(sf, smem_u32(Sb) + 2 * frag_b(lane, p0 + 16 * n, k, L::LN));
+            ldsm4(sf, smem_u32(Sb) + 2 * frag_b(lane, 16 * n, k, L::LN));
             mma_bf16(acc[2 * n], af, sf[0], sf[1]);
             mma_bf16(acc[2 * n + 1], af, sf[2], sf[3]);
           }
@@ -195,22 +200,23 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
               uint32_t xf[4];
-              ldsm4t(xf, ax + 2 * frag_bt(lane, p0 + 16 * n, 16 * k, L::LX));
+              ldsm4t(xf, ax + 2 * frag_bt(lane, 16 * n, 16 * k, L::LX));
               mma_bf16(acc[2 * n], mf, xf[0], xf[1]);
               mma_bf16(acc[2 * n + 1], mf, xf[2], xf[3]);
             }
           }
         }
-        // + D x, rows at or past the end are 0; through shared memory to 16-byte stores
-        __nv_bfloat16* yw = ys + wp * 16 * L::LY;
+        // + D x, rows at or past the end are 0; through shared memory to 16-byte stores, in
+        // the place of the warp's own rows of C, which no other warp reads
+        __syncwarp();
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
           const int e = 8 * n + 2 * q;
-          const uint32_t xa = *reinterpret_cast<const uint32_t*>(xs + ta * L::LX + p0 + e);
-          const uint32_t xb = *reinterpret_cast<const uint32_t*>(xs + tb * L::LX + p0 + e);
-          *reinterpret_cast<uint32_t*>(yw + g * L::LY + e) =
+          const uint32_t xa = *reinterpret_cast<const uint32_t*>(xs + ta * L::LX + e);
+          const uint32_t xb = *reinterpret_cast<const uint32_t*>(xs + tb * L::LX + e);
+          *reinterpret_cast<uint32_t*>(yw + g * L::LN + e) =
               ta < live ? pack_bf16(fmaf(Dh, bf16_lo(xa), acc[n][0]), fmaf(Dh, bf16_hi(xa), acc[n][1])) : 0u;
-          *reinterpret_cast<uint32_t*>(yw + (g + 8) * L::LY + e) =
+          *reinterpret_cast<uint32_t*>(yw + (g + 8) * L::LN + e) =
               tb < live ? pack_bf16(fmaf(Dh, bf16_lo(xb), acc[n][2]), fmaf(Dh, bf16_hi(xb), acc[n][3])) : 0u;
         }
         __syncwarp();
@@ -220,8 +226,8 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
         const int r = (lane >> 3) + 4 * i, t = t0 + 16 * rt + r;
         if (t < a.T) {
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (live > 16 * rt) v = *reinterpret_cast<const uint4*>(ys + (wp * 16 + r) * L::LY + (lane & 7) * 8);
-          *reinterpret_cast<uint4*>(y + row_off(a.sy, b, h, t) + p0 + (lane & 7) * 8) = v;
+          if (live > 16 * rt) v = *reinterpret_cast<const uint4*>(yw + r * L::LN + (lane & 7) * 8);
+          *reinterpret_cast<uint4*>(y + row_off(a.sy, b, h, t) + (lane & 7) * 8) = v;
         }
       }
     }
@@ -271,7 +277,7 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
     cp_async_commit();
   }
   cp_async_wait<0>();
-  float* out = OUT ? S + size_t(bh) * PN : slot;
+  float* out = OUT ? S + size_t(bh) * PN + size_t(pr) * N : slot;
   if (!OUT || a.nseg == 1) {
 #pragma unroll
     for (int n = 0; n < N / 8; ++n) {
@@ -280,39 +286,36 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
       *reinterpret_cast<float2*>(p0 + 8 * N) = make_float2(s[n][2], s[n][3]);
     }
   }
-  if (!OUT && tid == 0) segG[blockIdx.x] = tot;
+  if (!OUT && tid == 0 && pr == 0) segG[size_t(bh) * a.nseg + seg] = tot;
 }
 
-template <int P, int N>
+template <int N>
 static cudaError_t launch_tile(const SsmArgs& a, const void* x, const float* dt, const float* A,
                                const void* Bm, const void* Cm, const float* D, float* S,
                                const int32_t* lengths, void* y, float* segS, float* segG,
                                cudaStream_t s) {
   using bf = __nv_bfloat16;
-  const unsigned grid = unsigned(a.B * a.H) * unsigned(a.nseg);
-  const int s0 = int(SsmTile<P, N, false>::smem), s1 = int(SsmTile<P, N, true>::smem);
+  const unsigned grid = unsigned(a.B * a.H) * unsigned(a.P / 64) * unsigned(a.nseg);
+  const int s0 = int(SsmTile<N, false>::smem), s1 = int(SsmTile<N, true>::smem);
   auto go = [&](auto kernel, int sm) -> cudaError_t {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (r != cudaSuccess) return r;
-    kernel<<<grid, P * 2, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm, D, S, lengths,
-                                   (bf*)y, segS, segG);
+    kernel<<<grid, 128, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm, D, S, lengths, (bf*)y,
+                                 segS, segG);
     return cudaGetLastError();
   };
-  if (a.nseg == 1) return go(k_ssm_tile<P, N, true, 3>, s1);
-  cudaError_t e = go(k_ssm_tile<P, N, false, 3>, s0);
-  if (e == cudaSuccess) e = launch_ssm_carry(segS, segG, S, S, a.B * a.H, a.nseg, P * N, s);
-  return e == cudaSuccess ? go(k_ssm_tile<P, N, true, 2>, s1) : e;
+  if (a.nseg == 1) return go(k_ssm_tile<N, true, 3>, s1);
+  cudaError_t e = go(k_ssm_tile<N, false, 3>, s0);
+  if (e == cudaSuccess) e = launch_ssm_carry(segS, segG, S, S, a.B * a.H, a.nseg, a.P * N, s);
+  return e == cudaSuccess ? go(k_ssm_tile<N, true, 2>, s1) : e;
 }
 
 cudaError_t launch_ssm_fwd_mma(const SsmArgs& a, const void* x, const float* dt, const float* A,
                                const void* Bm, const void* Cm, const float* D, float* S,
                                const int32_t* lengths, void* y, float* segS, float* segG,
                                cudaStream_t s) {
-  if (a.P == 64)
-    return a.N == 64 ? launch_tile<64, 64>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s)
-                     : launch_tile<64, 128>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s);
-  return a.N == 64 ? launch_tile<128, 64>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s)
-                   : launch_tile<128, 128>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s);
+  return a.N == 64 ? launch_tile<64>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s)
+                   : launch_tile<128>(a, x, dt, A, Bm, Cm, D, S, lengths, y, segS, segG, s);
 }
 
 }  // namespace sdm

@@ -91,6 +91,22 @@ def test_select_long_and_ragged():
     assert (idx[1, :, :15] == -1).all()  # queries before the row's first key
 
 
+@pytest.mark.parametrize("d,block,n_sel,Tk", [(128, 32, 64, 9000), (64, 64, 16, 3000), (32, 32, 5, 5000)])
+def test_select_near_ties(d, block, n_sel, Tk):
+    """Scores that differ by less than float32 sums do, equal ones, large and tiny ones."""
+    q, k, _, g = _make(1, 8, 2, 300, Tk, d, BF)
+    kc = sdm.block_pool(k, block=block)
+    n = kc.shape[2]
+    kc[:, :, 1::3] = kc[:, :, 0:-1:3][:, :, :kc[:, :, 1::3].shape[2]]     # equal pairs
+    kc[:, :, 2::3, 0] = kc[:, :, 2::3, 0] * 1.0078125                     # one step of one element
+    q[:, :, 100:150] *= 2.0 ** 60
+    q[:, :, 150:200] *= 2.0 ** -100
+    q[:, 1:4, 200:250] = -q[:, :1, 200:250] * 0.99609375                  # heads that cancel
+    kc[:, 1, n // 2] *= 1000                                              # one long mean
+    idx = sdm.block_select(q, kc, n_sel=n_sel, block=block, Tk=Tk)
+    assert torch.equal(idx, R.select(q, kc, n_sel, block, Tk))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_select_ties_and_non_finite(dtype):
     q, k, _, _ = _make(1, 2, 1, 600, 600, 64, dtype)
