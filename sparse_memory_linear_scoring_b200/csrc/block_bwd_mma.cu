@@ -5,8 +5,11 @@
 // memory and dK and dV in registers while the rows stream past, 64 at a time:
 //     P = exp(scale Q K^T - lse),  dS = P (dO V^T - delta) scale,
 //     dV += P^T dO,  dK += dS^T Q,  dQ part = dS K.
-// P and dS are rounded to bf16 once for the second products (2^-9 of a term, as the
-// results themselves).  Each warp owns 16 rows for P, dS and dQ, and 16 keys (or 16 keys
+// P and dS are rounded to bf16 once for dV and dK (2^-9 of a term, as the results
+// themselves).  dQ takes dS in two bf16 parts (2^-17): a row of dS sums to zero, so what its
+// keys have in common drops out of dQ, while rounding errors times it do not (0.0038 of
+// the norm off with one part, 0.0024 with two, 0.0017 of it the result's own rounding).
+// Each warp owns 16 rows for P, dS and dQ, and 16 keys (or 16 keys
 // and half the columns) for dK and dV, whose operands it takes transposed from shared
 // memory.  A row's dQ is a sum over its list: parts are halves scaled by their
 // largest element (2^-12 beside the result's 2^-9), joined in list order.  dK and dV of
@@ -29,7 +32,7 @@ struct GradTile {
   static constexpr int ST = D <= 64 ? 2 : 1;   // row tiles in flight; at 128 a second CTA an SM does more
   static constexpr int LD = D + 8, LP = KT + 8;
   static constexpr int KV = KT * LD, RW = kGradTile * LD, PS = kGradTile * LP;
-  static constexpr size_t smem = size_t(2) * (2 * KV + ST * 2 * RW + 2 * PS) + 16;
+  static constexpr size_t smem = size_t(2) * (2 * KV + ST * 2 * RW + 3 * PS) + 16;
 };
 
 template <int D, int KT>
@@ -44,7 +47,8 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
   __nv_bfloat16* Rs = Vs + L::KV;                  // [ST][Q, dO][64][LD]
   __nv_bfloat16* Ps = Rs + L::ST * 2 * L::RW;      // [64][LP]
   __nv_bfloat16* Ds = Ps + L::PS;
-  uint32_t* odd = reinterpret_cast<uint32_t*>(Ds + L::PS);  // keys with inf or NaN in K
+  __nv_bfloat16* Es = Ds + L::PS;                  // second part of dS
+  uint32_t* odd = reinterpret_cast<uint32_t*>(Es + L::PS);  // keys with inf or NaN in K
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   const int g = lane >> 2, qd = lane & 3;
   const int per = a.bs / KT, sub = blockIdx.x % per;
@@ -115,7 +119,7 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
   __syncthreads();
   const bool anyodd = (odd[0] | odd[KT / 32 - 1]) != 0;
   const float c2 = a.scale * kLog2e;
-  const uint32_t ak = smem_u32(Ks), av = smem_u32(Vs), ap = smem_u32(Ps), ad = smem_u32(Ds);
+  const uint32_t ak = smem_u32(Ks), av = smem_u32(Vs), ap = smem_u32(Ps), ad = smem_u32(Ds), ae = smem_u32(Es);
   // dK, dV: keys 16 ks.., columns cp DP..
   constexpr int NK = KT / 16, DP = D * NK / 4;
   const int ks = wp % NK, cp = (wp / NK) * DP;
@@ -137,7 +141,6 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     __syncwarp();
     const __nv_bfloat16* Qs = Rs + st * 2 * L::RW;
     const uint32_t aq = smem_u32(Qs), ao = aq + 2 * L::RW;
-    uint32_t df[KT / 16][4];  // dS as an A operand
     {
       float sc[KT / 8][4], dp[KT / 8][4];
 #pragma unroll
@@ -174,13 +177,15 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
           if (masked && col >= nb) p[2 + i] = s[2 + i] = 0.f;
         }
         const int at = (16 * wp + g) * L::LP + 8 * n + 2 * qd;
-        const uint32_t s0 = pack_bf16(s[0], s[1]), s1 = pack_bf16(s[2], s[3]);
-        df[n >> 1][(n & 1) * 2] = s0;
-        df[n >> 1][(n & 1) * 2 + 1] = s1;
+        uint32_t s0[2], s1[2];
+        split_bf16<2>(s[0], s[1], s0);
+        split_bf16<2>(s[2], s[3], s1);
         *reinterpret_cast<uint32_t*>(Ps + at) = pack_bf16(p[0], p[1]);
         *reinterpret_cast<uint32_t*>(Ps + at + 8 * L::LP) = pack_bf16(p[2], p[3]);
-        *reinterpret_cast<uint32_t*>(Ds + at) = s0;
-        *reinterpret_cast<uint32_t*>(Ds + at + 8 * L::LP) = s1;
+        *reinterpret_cast<uint32_t*>(Ds + at) = s0[0];
+        *reinterpret_cast<uint32_t*>(Ds + at + 8 * L::LP) = s1[0];
+        *reinterpret_cast<uint32_t*>(Es + at) = s0[1];
+        *reinterpret_cast<uint32_t*>(Es + at + 8 * L::LP) = s1[1];
       }
     }
     __syncthreads();  // all rows' Q, dO, P and dS are in place
@@ -207,37 +212,39 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     if (!anyodd) {
 #pragma unroll
-      for (int kk = 0; kk < KT / 16; ++kk)
+      for (int kk = 0; kk < KT / 16; ++kk) {
+        uint32_t df[4], ef[4];
+        ldsm4(df, ad + 2 * frag_a(lane, 16 * wp, 16 * kk, L::LP));
+        ldsm4(ef, ae + 2 * frag_a(lane, 16 * wp, 16 * kk, L::LP));
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) {
           uint32_t bf[4];
           ldsm4t(bf, ak + 2 * frag_bt(lane, 16 * n, 16 * kk, L::LD));
-          mma_bf16(acc[2 * n], df[kk], bf[0], bf[1]);
-          mma_bf16(acc[2 * n + 1], df[kk], bf[2], bf[3]);
+          mma_bf16(acc[2 * n], ef, bf[0], bf[1]);
+          mma_bf16(acc[2 * n + 1], ef, bf[2], bf[3]);
+          mma_bf16(acc[2 * n], df, bf[0], bf[1]);
+          mma_bf16(acc[2 * n + 1], df, bf[2], bf[3]);
         }
+      }
     } else {
       // 0 times an infinite or NaN key is not 0: keys that a row does not see are left out by hand
+      for (int key = 0; key < KT; ++key) {
+        const int pa = (16 * wp + g) * L::LP + key, pb = pa + 8 * L::LP;
+        const float xa = __bfloat162float(Ds[pa]) + __bfloat162float(Es[pa]);
+        const float xb = __bfloat162float(Ds[pb]) + __bfloat162float(Es[pb]);
 #pragma unroll
-      for (int kk = 0; kk < KT / 16; ++kk)
-        for (int y = 0; y < 16; ++y) {
-          const int src = (lane & ~3) | ((y >> 1) & 3);
-          const uint32_t wa = __shfl_sync(0xffffffffu, y < 8 ? df[kk][0] : df[kk][2], src);
-          const uint32_t wb = __shfl_sync(0xffffffffu, y < 8 ? df[kk][1] : df[kk][3], src);
-          const float xa = (y & 1) ? bf16_hi(wa) : bf16_lo(wa), xb = (y & 1) ? bf16_hi(wb) : bf16_lo(wb);
-          const int key = 16 * kk + y;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(Ks + key * L::LD + 8 * n + 2 * qd);
-            if (key < na) {
-              acc[n][0] = fmaf(xa, bf16_lo(u), acc[n][0]);
-              acc[n][1] = fmaf(xa, bf16_hi(u), acc[n][1]);
-            }
-            if (key < nb) {
-              acc[n][2] = fmaf(xb, bf16_lo(u), acc[n][2]);
-              acc[n][3] = fmaf(xb, bf16_hi(u), acc[n][3]);
-            }
+        for (int n = 0; n < D / 8; ++n) {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(Ks + key * L::LD + 8 * n + 2 * qd);
+          if (key < na) {
+            acc[n][0] = fmaf(xa, bf16_lo(u), acc[n][0]);
+            acc[n][1] = fmaf(xa, bf16_hi(u), acc[n][1]);
+          }
+          if (key < nb) {
+            acc[n][2] = fmaf(xb, bf16_lo(u), acc[n][2]);
+            acc[n][3] = fmaf(xb, bf16_hi(u), acc[n][3]);
           }
         }
+      }
     }
     float xa = 0.f, xb = 0.f;
 #pragma unroll
