@@ -7,8 +7,8 @@
 //     dV += P^T dO,  dK += dS^T Q,  dQ part = dS K.
 // P and dS are rounded to bf16 once for dV and dK (2^-9 of a term, as the results
 // themselves).  dQ takes dS in two bf16 parts (2^-17): a row of dS sums to zero, so what its
-// keys have in common drops out of dQ, while rounding errors times it do not (0.0038 of
-// the norm off with one part, 0.0024 with two, 0.0017 of it the result's own rounding).
+// keys have in common drops out of dQ, while rounding errors times it do not (0.0026 of the
+// norm; the result's own rounding is 0.0017).
 // Each warp owns 16 rows for P, dS and dQ, and 16 keys (or 16 keys
 // and half the columns) for dK and dV, whose operands it takes transposed from shared
 // memory.  A row's dQ is a sum over its list: parts are halves scaled by their
@@ -17,6 +17,9 @@
 // bits.  Without the parts a row's dQ would need a second walk over its list, which
 // reads K and V once more per query and recomputes P and dS, about half of all products.
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "block_internal.cuh"
 #include "mma_dev.cuh"
@@ -141,6 +144,7 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     __syncwarp();
     const __nv_bfloat16* Qs = Rs + st * 2 * L::RW;
     const uint32_t aq = smem_u32(Qs), ao = aq + 2 * L::RW;
+    float ea = 0.f, eb = 0.f;  // the rows' sums of dS
     {
       float sc[KT / 8][4], dp[KT / 8][4];
 #pragma unroll
@@ -177,6 +181,8 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
           if (masked && col >= nb) p[2 + i] = s[2 + i] = 0.f;
         }
         const int at = (16 * wp + g) * L::LP + 8 * n + 2 * qd;
+        ea += s[0] + s[1];
+        eb += s[2] + s[3];
         uint32_t s0[2], s1[2];
         split_bf16<2>(s[0], s[1], s0);
         split_bf16<2>(s[2], s[3], s1);
@@ -210,39 +216,49 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    if (!anyodd) {
+    // acc += (A, and A2 beside it) K; `clean` leaves out what is not finite in K, since 0
+    // times that is not 0
+    auto times_keys = [&](auto clean, auto two, uint32_t a1, uint32_t a2) {
 #pragma unroll
       for (int kk = 0; kk < KT / 16; ++kk) {
         uint32_t df[4], ef[4];
-        ldsm4(df, ad + 2 * frag_a(lane, 16 * wp, 16 * kk, L::LP));
-        ldsm4(ef, ae + 2 * frag_a(lane, 16 * wp, 16 * kk, L::LP));
+        ldsm4(df, a1 + 2 * frag_a(lane, 16 * wp, 16 * kk, L::LP));
+        if constexpr (decltype(two)::value) ldsm4(ef, a2 + 2 * frag_a(lane, 16 * wp, 16 * kk, L::LP));
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) {
           uint32_t bf[4];
           ldsm4t(bf, ak + 2 * frag_bt(lane, 16 * n, 16 * kk, L::LD));
-          mma_bf16(acc[2 * n], ef, bf[0], bf[1]);
-          mma_bf16(acc[2 * n + 1], ef, bf[2], bf[3]);
+          if constexpr (decltype(clean)::value) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((bf[i] & 0x7f80u) == 0x7f80u) bf[i] &= 0xffff0000u;
+              if ((bf[i] & 0x7f800000u) == 0x7f800000u) bf[i] &= 0x0000ffffu;
+            }
+          }
+          if constexpr (decltype(two)::value) {
+            mma_bf16(acc[2 * n], ef, bf[0], bf[1]);
+            mma_bf16(acc[2 * n + 1], ef, bf[2], bf[3]);
+          }
           mma_bf16(acc[2 * n], df, bf[0], bf[1]);
           mma_bf16(acc[2 * n + 1], df, bf[2], bf[3]);
         }
       }
-    } else {
-      // 0 times an infinite or NaN key is not 0: keys that a row does not see are left out by hand
+    };
+    if (D == 128 || anyodd) times_keys(std::true_type(), std::true_type(), ad, ae);  // one copy: registers
+    else times_keys(std::false_type(), std::true_type(), ad, ae);
+    if (anyodd) {  // the rest of the keys that are not finite, for the rows that see them
       for (int key = 0; key < KT; ++key) {
+        if (!(odd[key >> 5] >> (key & 31) & 1)) continue;
         const int pa = (16 * wp + g) * L::LP + key, pb = pa + 8 * L::LP;
-        const float xa = __bfloat162float(Ds[pa]) + __bfloat162float(Es[pa]);
-        const float xb = __bfloat162float(Ds[pb]) + __bfloat162float(Es[pb]);
+        const float xa = __bfloat162float(Ds[pa]), xb = __bfloat162float(Ds[pb]);
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) {
           const uint32_t u = *reinterpret_cast<const uint32_t*>(Ks + key * L::LD + 8 * n + 2 * qd);
-          if (key < na) {
-            acc[n][0] = fmaf(xa, bf16_lo(u), acc[n][0]);
-            acc[n][1] = fmaf(xa, bf16_hi(u), acc[n][1]);
-          }
-          if (key < nb) {
-            acc[n][2] = fmaf(xb, bf16_lo(u), acc[n][2]);
-            acc[n][3] = fmaf(xb, bf16_hi(u), acc[n][3]);
-          }
+          const bool lo = (u & 0x7f80u) == 0x7f80u, hi = (u & 0x7f800000u) == 0x7f800000u;
+          if (lo && key < na) acc[n][0] = fmaf(xa, bf16_lo(u), acc[n][0]);
+          if (hi && key < na) acc[n][1] = fmaf(xa, bf16_hi(u), acc[n][1]);
+          if (lo && key < nb) acc[n][2] = fmaf(xb, bf16_lo(u), acc[n][2]);
+          if (hi && key < nb) acc[n][3] = fmaf(xb, bf16_hi(u), acc[n][3]);
         }
       }
     }
@@ -270,10 +286,10 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     xa = fmaxf(xa, 2.3509887e-38f);  // 2^-125: its reciprocal is still finite
     xb = fmaxf(xb, 2.3509887e-38f);
     const float va = 1.f / xa, vb = 1.f / xb;
-    const size_t oa = __shfl_sync(0xffffffffu, me.place, g), ob = __shfl_sync(0xffffffffu, me.place, g + 8);
-    if (qd == 0) {
-      if (ra < r1) w.mul[oa] = xa;
-      if (rb < r1) w.mul[ob] = xb;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      ea += __shfl_xor_sync(0xffffffffu, ea, o);
+      eb += __shfl_xor_sync(0xffffffffu, eb, o);
     }
     __syncthreads();  // everyone has read this tile's rows, P and dS
     __half* stage = reinterpret_cast<__half*>(Rs + st * 2 * L::RW + wp * 16 * L::LD);
@@ -292,6 +308,50 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
       const size_t u = __shfl_sync(0xffffffffu, me.place, r);
       if (base + 16 * wp + r < r1)
         *reinterpret_cast<uint4*>(part + u * D + c) = *reinterpret_cast<const uint4*>(stage + r * L::LD + c);
+    }
+    // sum P_k k_k, as above, over what is finite (a row that sees more has no finite dQ)
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    if (D == 128 || anyodd) times_keys(std::true_type(), std::false_type(), ap, ap);
+    else times_keys(std::false_type(), std::false_type(), ap, ap);
+    float ka = 0.f, kb = 0.f;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      ka = fmaxf(ka, fmaxf(fabsf(acc[n][0]), fabsf(acc[n][1])));
+      kb = fmaxf(kb, fmaxf(fabsf(acc[n][2]), fabsf(acc[n][3])));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
+      kb = fmaxf(kb, __shfl_xor_sync(0xffffffffu, kb, o));
+    }
+    ka = fminf(fmaxf(ka, 2.3509887e-38f), 1.7e38f);
+    kb = fminf(fmaxf(kb, 2.3509887e-38f), 1.7e38f);
+    const float fa = 1.f / ka, fb = 1.f / kb;
+    const size_t oa = __shfl_sync(0xffffffffu, me.place, g), ob = __shfl_sync(0xffffffffu, me.place, g + 8);
+    if (qd == 0) {
+      if (ra < r1) w.mul[oa] = make_float4(xa, ka, ea, 0.f);
+      if (rb < r1) w.mul[ob] = make_float4(xb, kb, eb, 0.f);
+    }
+    __syncwarp();  // the warp has sent its parts of dQ
+    unsigned short* bytes = reinterpret_cast<unsigned short*>(stage);  // rows of LD halves again
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      bytes[g * L::LD + 4 * n + qd] =
+          __nv_cvt_float2_to_fp8x2(make_float2(acc[n][0] * fa, acc[n][1] * fa), __NV_SATFINITE, __NV_E4M3);
+      bytes[(g + 8) * L::LD + 4 * n + qd] =
+          __nv_cvt_float2_to_fp8x2(make_float2(acc[n][2] * fb, acc[n][3] * fb), __NV_SATFINITE, __NV_E4M3);
+    }
+    __syncwarp();
+    unsigned char* kpart = static_cast<unsigned char*>(w.kpart);
+#pragma unroll
+    for (int i = lane; i < 16 * (D / 16); i += 32) {
+      const int r = i / (D / 16), c = (i % (D / 16)) * 16;
+      const size_t u = __shfl_sync(0xffffffffu, me.place, r);
+      if (base + 16 * wp + r < r1)
+        *reinterpret_cast<uint4*>(kpart + u * D + c) = *reinterpret_cast<const uint4*>(bytes + r * L::LD + c / 2);
     }
     __syncwarp();  // before the next fetch into these rows
     if (L::ST == 1 && base + kGradTile < r1) fetch(base + kGradTile, 0, next);
@@ -332,9 +392,10 @@ k_blk_delta(BlkArgs a, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16*
 }
 
 // A row of dq from its parts, in list order; pairs without keys have none.  As in the
-// forward's join a lane looks up every LN-th part, and 4 rows' loads are in flight.
+// forward's join a lane looks up every LN-th part; two rows' loads are in flight (four
+// take registers that more warps use better).
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 5)
 k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ dq,
          sdm_strides sdq, int kt) {
   constexpr int LN = D / 8;
@@ -347,34 +408,55 @@ k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* 
   const int32_t* list = idx + ((size_t)bg * a.Tq + a.q0 + t) * a.n_sel;
   const int p = blk_pos0(a, b) + a.q0 + t, parts = a.n_sel * per;
   // part y: slot y / per, keys (y % per) kt .. of its block
-  auto place = [&](int y) {
-    const int s = per == 2 ? y >> 1 : y;
-    return (((size_t)bt * a.n_sel + s) * a.R + r) * per + (per == 2 ? y & 1 : 0);
+  auto place = [&](int y) { return per == 2 ? (y >> 1) * 2 * a.R + (y & 1) : y * a.R; };
+  const size_t first = ((size_t)bt * a.n_sel * a.R + r) * per;
+  const __half* part = static_cast<const __half*>(w.part) + first * D + c;
+  const unsigned char* kpart = static_cast<const unsigned char*>(w.kpart) + first * D + c;
+  const float4* mul = w.mul + first;
+  auto there = [&](int y) {
+    return y < parts && blk_keys(a, list[per == 2 ? y >> 1 : y], p) > (per == 2 && (y & 1) ? kt : 0);
   };
-  const __half* part = static_cast<const __half*>(w.part) + c;
+  float e = 0.f;
+  for (int y = ln; y < parts; y += LN)
+    if (there(y)) e += mul[place(y)].z;
+#pragma unroll
+  for (int z = 1; z < LN; z <<= 1) e += __shfl_xor_sync(0xffffffffu, e, z);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int y0 = 0; y0 < parts; y0 += LN) {
-    const int y = y0 + ln;
-    float f = -1.f;  // no part
-    if (y < parts && blk_keys(a, list[per == 2 ? y >> 1 : y], p) > (per == 2 && (y & 1) ? kt : 0)) f = w.mul[place(y)];
+    float f = -1.f, fk = 0.f;  // no part
+    if (there(y0 + ln)) {
+      const float4 u = mul[place(y0 + ln)];
+      f = u.x;
+      fk = -e * u.y;
+    }
 #pragma unroll
-    for (int z0 = 0; z0 < LN; z0 += 4) {
-      uint4 x[4];
-      float fz[4];
+    for (int z0 = 0; z0 < LN; z0 += 2) {
+      uint4 x[2];
+      uint2 kx[2];
+      float fz[2], kz[2];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
+      for (int z = 0; z < 2; ++z) {
         fz[z] = __shfl_sync(0xffffffffu, f, z0 + z, LN);
+        kz[z] = __shfl_sync(0xffffffffu, fk, z0 + z, LN);
         x[z] = make_uint4(0u, 0u, 0u, 0u);
-        if (fz[z] != -1.f) x[z] = *reinterpret_cast<const uint4*>(part + place(y0 + z0 + z) * D);
+        kx[z] = make_uint2(0u, 0u);
+        if (fz[z] != -1.f) {
+          const int at = place(y0 + z0 + z) * D;
+          x[z] = *reinterpret_cast<const uint4*>(part + at);
+          if (kz[z] != 0.f) kx[z] = *reinterpret_cast<const uint2*>(kpart + at);
+        }
       }
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
+      for (int z = 0; z < 2; ++z) {
         const __half2* hx = reinterpret_cast<const __half2*>(&x[z]);
+        const unsigned short* k8 = reinterpret_cast<const unsigned short*>(&kx[z]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float2 v = __half22float2(hx[u]);
-          acc[2 * u] = fmaf(fz[z], v.x, acc[2 * u]);
-          acc[2 * u + 1] = fmaf(fz[z], v.y, acc[2 * u + 1]);
+          const __half2_raw kr = __nv_cvt_fp8x2_to_halfraw2(k8[u], __NV_E4M3);
+          const float2 kv = __half22float2(__half2(kr));
+          acc[2 * u] = fmaf(kz[z], kv.x, fmaf(fz[z], v.x, acc[2 * u]));
+          acc[2 * u + 1] = fmaf(kz[z], kv.y, fmaf(fz[z], v.y, acc[2 * u + 1]));
         }
       }
     }
@@ -427,7 +509,7 @@ bool blk_bwd_tiles_pay(const sdm_block_dims* d) { return d->in_dtype == SDM_DTYP
 
 // Queries per pass: as many as keep the parts of dq within 2 GiB (at least 128).
 int blk_bwd_chunk(const sdm_block_dims* d) {
-  const long long per = (long long)d->B * d->H * d->n_sel * (d->block / grad_keys(d)) * (d->d * 2 + 4);
+  const long long per = (long long)d->B * d->H * d->n_sel * (d->block / grad_keys(d)) * (d->d * 3 + 16);
   long long n = (2LL << 30) / per;
   if (n < 128) n = 128;
   if (n > d->Tq) n = d->Tq;
@@ -453,8 +535,9 @@ BlkBwdWs blk_bwd_ws(const sdm_block_dims* d, int nq, void* base) {
   w.sum = reinterpret_cast<float*>(take(blk_bwd_chunk(d) < d->Tq ? 2 * BG * d->Tk * d->d * 4 : 0));
   w.plan = blk_plan(d, nq, kGradRows, b + o);
   take(w.plan.bytes);
-  w.mul = reinterpret_cast<float*>(take(rows * 4));
+  w.mul = reinterpret_cast<float4*>(take(rows * 16));
   w.part = take(rows * d->d * 2);
+  w.kpart = take(rows * d->d);
   w.kv = reinterpret_cast<float*>(take(BG * w.plan.most * d->block * 2 * d->d * 4));
   w.bytes = o;
   return w;

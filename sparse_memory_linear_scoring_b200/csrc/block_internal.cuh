@@ -107,8 +107,9 @@ struct BlkBwdWs {
   float* delta;    // [B][H][Tq] do.o
   float* sum;      // [2][BG][Tk][d] dk, dv so far, where there is more than one pass
   BlkPlan plan;
-  float* mul;      // [BG][nq][n_sel][R][block / keys] scale of each part of dq
-  void* part;      // [BG][nq][n_sel][R][block / keys][d] half
+  float4* mul;     // [BG][nq][n_sel][R][block / keys] scales of each part of dq and of sum P k, sum of dS
+  void* part;      // [BG][nq][n_sel][R][block / keys][d] half: dq
+  void* kpart;     // [BG][nq][n_sel][R][block / keys][d] e4m3: sum P k
   float* kv;       // [BG][items][block / keys][2][keys][d] parts of dk, dv
   size_t bytes;
 };
