@@ -5,17 +5,23 @@
 // memory and dK and dV in registers while the rows stream past, 64 at a time:
 //     P = exp(scale Q K^T - lse),  dS = P (dO V^T - delta) scale,
 //     dV += P^T dO,  dK += dS^T Q,  dQ part = dS K.
-// P and dS are rounded to bf16 once for dV and dK (2^-9 of a term, as the results
-// themselves).  dQ takes dS in two bf16 parts (2^-17): a row of dS sums to zero, so what its
-// keys have in common drops out of dQ, while rounding errors times it do not (0.0026 of the
-// norm; the result's own rounding is 0.0017).
-// Each warp owns 16 rows for P, dS and dQ, and 16 keys (or 16 keys
-// and half the columns) for dK and dV, whose operands it takes transposed from shared
-// memory.  A row's dQ is a sum over its list: parts are halves scaled by their
-// largest element (2^-12 beside the result's 2^-9), joined in list order.  dK and dV of
-// one item are float32 parts, joined in item order: no atomics, equal calls give equal
-// bits.  Without the parts a row's dQ would need a second walk over its list, which
-// reads K and V once more per query and recomputes P and dS, about half of all products.
+// P is rounded to bf16 once for dV (2^-9 of a term, as the result itself).  dQ and dK take
+// dS in two bf16 parts (2^-17): a row of dS sums to zero, so what its keys (for dK: a key's
+// queries) have in common drops out, while rounding errors times it do not (0.0026 of dQ's
+// norm; the result's own rounding is 0.0017).  Each warp owns 16 rows for P, dS and dQ, and
+// 16 keys (or 16 keys and half the columns) for dK and dV, whose operands it takes
+// transposed from shared memory.  A row's dQ is a sum over its list: parts are halves
+// scaled by their largest element (2^-12 beside the result's 2^-9), joined in list order.
+// dK and dV of one item are float32 parts, joined in item order: no atomics, equal calls
+// give equal bits.
+// delta = do.o comes from o as the forward wrote it, in bf16, and what that is off, e, is
+// off in dQ by e sum_k P_k k_k: the largest error there would be (0.0022 of the norm).  But
+// sum_k dS_k over a row's list is e scale instead of 0, so each part also leaves its sum
+// of dS and its sum P_k k_k (8-bit floats over a power of two: a factor of an error), and
+// the join takes their product off again.
+// Without the parts a row's dQ would need a second walk over its list, which reads K and
+// V once more per query and recomputes P and dS, about half of all products.
+// 4 x 2048 tokens, 8 heads of 64 on 2, 8 blocks of 64: 155 us here, 33 for the join of dQ.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -197,9 +203,10 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
     __syncthreads();  // all rows' Q, dO, P and dS are in place
 #pragma unroll
     for (int kk = 0; kk < kGradTile; kk += 16) {
-      uint32_t pf[4], sf[4];
+      uint32_t pf[4], sf[4], tf[4];
       ldsm4t(pf, ap + 2 * frag_at(lane, 16 * ks, kk, L::LP));
       ldsm4t(sf, ad + 2 * frag_at(lane, 16 * ks, kk, L::LP));
+      ldsm4t(tf, ae + 2 * frag_at(lane, 16 * ks, kk, L::LP));
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
         uint32_t bf[4];
@@ -207,6 +214,8 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
         mma_bf16(gv[2 * n], pf, bf[0], bf[1]);
         mma_bf16(gv[2 * n + 1], pf, bf[2], bf[3]);
         ldsm4t(bf, aq + 2 * frag_bt(lane, cp + 16 * n, kk, L::LD));
+        mma_bf16(gk[2 * n], tf, bf[0], bf[1]);
+        mma_bf16(gk[2 * n + 1], tf, bf[2], bf[3]);
         mma_bf16(gk[2 * n], sf, bf[0], bf[1]);
         mma_bf16(gk[2 * n + 1], sf, bf[2], bf[3]);
       }
@@ -466,10 +475,10 @@ k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* 
 
 // dk, dv of 4 columns of a key: the items of its block in order.  With several passes
 // over the queries, sum [2][BG][nb * block][D] carries the total from pass to pass.
-template <int D>
+template <typename Tin, int D>
 __global__ void __launch_bounds__(256)
-k_blk_dkv(BlkArgs a, BlkBwdWs w, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
-          sdm_strides sdk, sdm_strides sdv, int kt, int begin, int end) {
+k_blk_dkv(BlkArgs a, BlkBwdWs w, Tin* __restrict__ dk, Tin* __restrict__ dv,
+          sdm_strides sdk, sdm_strides sdv, int kt, int begin, int end, int vec) {
   constexpr int LN = D / 4;
   long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const int c = int(i % LN) * 4;
@@ -495,9 +504,34 @@ k_blk_dkv(BlkArgs a, BlkBwdWs w, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* 
   } else {
     const float f[4] = {s.x, s.y, s.z, s.w};
     const int b = bg / a.G, g = bg - b * a.G;
-    __nv_bfloat16* o = which ? dv + row_off(sdv, b, g, key) : dk + row_off(sdk, b, g, key);
-    Vec<__nv_bfloat16, 4>::store(o + c, f);
+    Tin* o = which ? dv + row_off(sdv, b, g, key) : dk + row_off(sdk, b, g, key);
+    if (vec) {
+      Vec<Tin, 4>::store(o + c, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c + e] = from_f32<Tin>(f[e]);
+    }
   }
+}
+
+cudaError_t launch_blk_dkv(const BlkArgs& a, const BlkBwdWs& w, bool bf16, void* dk, void* dv,
+                           const sdm_strides& sdk, const sdm_strides& sdv, int kt, bool begin, bool end,
+                           cudaStream_t s) {
+  const long long n = (long long)a.B * a.G * a.Tk * (a.d / 4);
+  const dim3 grid(unsigned((n + 255) / 256), 2);
+  const int es = bf16 ? 2 : 4;
+  const int vec = view_aligned(dk, sdk, es, 4 * es) && view_aligned(dv, sdv, es, 4 * es);
+  auto go = [&](auto dd) {
+    constexpr int D = decltype(dd)::value;
+    if (bf16)
+      k_blk_dkv<__nv_bfloat16, D><<<grid, 256, 0, s>>>(a, w, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, sdk, sdv,
+                                                       kt, begin, end, vec);
+    else
+      k_blk_dkv<float, D><<<grid, 256, 0, s>>>(a, w, (float*)dk, (float*)dv, sdk, sdv, kt, begin, end, vec);
+    return cudaGetLastError();
+  };
+  return a.d == 32 ? go(std::integral_constant<int, 32>())
+                   : a.d == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
 }
 
 // ---------------------------------------------------------------- host side
@@ -576,10 +610,9 @@ static cudaError_t launch_grad(const sdm_block_dims* d, BlkArgs a, const void* q
     if (e != cudaSuccess) return e;
     const long long nr = (long long)a.B * a.H * a.nq * (D / 8);
     k_blk_dq<D><<<unsigned((nr + 255) / 256), 256, 0, s>>>(a, w, idx, (bf*)dq, gv->q, kt);
-    const long long nk = (long long)a.B * a.G * a.Tk * (D / 4);
-    k_blk_dkv<D><<<dim3(unsigned((nk + 255) / 256), 2), 256, 0, s>>>(
-        a, w, (bf*)dk, (bf*)dv, gv->k, gv->v, kt, q0 == 0, q0 + a.nq == d->Tq);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_blk_dkv(a, w, true, dk, dv, gv->k, gv->v, kt, q0 == 0, q0 + a.nq == d->Tq, s);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

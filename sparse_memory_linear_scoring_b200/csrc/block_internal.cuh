@@ -116,6 +116,10 @@ struct BlkBwdWs {
 BlkBwdWs blk_bwd_ws(const sdm_block_dims* d, int nq, void* base);
 bool blk_bwd_tiles_pay(const sdm_block_dims* d);
 int blk_bwd_chunk(const sdm_block_dims* d);
+// dk, dv from the items' parts w.kv of kt keys each (with begin and end: of one pass).
+cudaError_t launch_blk_dkv(const BlkArgs& a, const BlkBwdWs& w, bool bf16, void* dk, void* dv,
+                           const sdm_strides& sdk, const sdm_strides& sdv, int kt, bool begin, bool end,
+                           cudaStream_t s);
 cudaError_t launch_blk_bwd_mma(const sdm_block_dims* d, BlkArgs a, const void* q, const void* k,
                                const void* v, const int32_t* idx, const void* o, const float* lse,
                                const void* d_o, void* dq, void* dk, void* dv,

@@ -5,10 +5,11 @@
 // and to their gradients, and, after the carries, the gradients.  What ends in float32
 // (states, ddt, dA, dD, dS0) keeps float32 accuracy: products of bf16 inputs are exact,
 // and a float32 operand beside a bf16 one is split into three bf16 parts (rest below
-// 2^-24).  The weights W G and W dt R, whose products end in bf16, are rounded once.
-// Per chunk and head 12 products of 64 x 64 x 64 at widths of 64, six of them for the
-// splits; the tiles of x, dy, B, C and the two float32 states that a CTA reads (72 KB)
-// bound it.
+// 2^-24).  W G, whose product ends in dx, is rounded once; W dt R is two parts: in
+// a short call it makes most of dB and dC, and one part's error (0.0021 of their norm) would
+// add to the results' own (0.0017).  Per chunk and head 14 products of 64 x 64 x 64 at
+// widths of 64, eight of them for the splits; the tiles of x, dy, B, C and the two float32
+// states that a CTA reads (72 KB) bound it.
 #include "mma_dev.cuh"
 #include "ssm_internal.cuh"
 
@@ -134,8 +135,8 @@ template <int P, int N>
 struct SsmGradTile {
   static constexpr int LX = P + 8, LN = N + 8, LM = kGQ + 8;
   static constexpr int SP = P * LN;  // one part of a state
-  // x, dy, B, C; three parts of one state at a time; the weights W G, W dt R
-  static constexpr int elems = 2 * kGQ * (LX + LN) + 3 * SP + 2 * kGQ * LM;
+  // x, dy, B, C; three parts of one state at a time; the weights W G, W dt R in two parts
+  static constexpr int elems = 2 * kGQ * (LX + LN) + 3 * SP + 3 * kGQ * LM;
   // decays [5][64], row sums of E and dots with C, B [2][3][64], column sums [4][64],
   // boundary [8], R_tt [64]
   static constexpr int floats = 5 * kGQ + 6 * kGQ + 4 * kGQ + kGQ + 8;
@@ -178,7 +179,8 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
   __nv_bfloat16* Ss = Cs + kGQ * L::LN;
   __nv_bfloat16* MG = Ss + 3 * L::SP;
   __nv_bfloat16* MR = MG + kGQ * L::LM;
-  float* dec = reinterpret_cast<float*>(MR + kGQ * L::LM);
+  __nv_bfloat16* M2 = MR + kGQ * L::LM;
+  float* dec = reinterpret_cast<float*>(M2 + kGQ * L::LM);
   const float *hi = dec, *lo = dec + kGQ, *dts = dec + 2 * kGQ, *eg = dec + 3 * kGQ, *ej = dec + 4 * kGQ;
   float* rowE = dec + 5 * kGQ;   // [2][64]
   float* dotC = rowE + 2 * kGQ;  // [2][64] C_t.I1_t
@@ -187,7 +189,7 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
   float* dg = colE + 4 * kGQ;    // [64] R_tt
   float* red = dg + kGQ;         // [8]
   const uint32_t ax = smem_u32(xs), ay = smem_u32(ys), ab = smem_u32(Bs), ac = smem_u32(Cs),
-                 as = smem_u32(Ss), ag = smem_u32(MG), ar = smem_u32(MR);
+                 as = smem_u32(Ss), ag = smem_u32(MG), ar = smem_u32(MR), a2 = smem_u32(M2);
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int rt = wp & 3, ch = wp >> 2;
   const int c = blockIdx.x % a.nch, bh = blockIdx.x / a.nch;
@@ -262,8 +264,13 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
       }
       *reinterpret_cast<uint32_t*>(MG + ta * L::LM + j) = pack_bf16(mg[0], mg[1]);
       *reinterpret_cast<uint32_t*>(MG + tb * L::LM + j) = pack_bf16(mg[2], mg[3]);
-      *reinterpret_cast<uint32_t*>(MR + ta * L::LM + j) = pack_bf16(mr[0], mr[1]);
-      *reinterpret_cast<uint32_t*>(MR + tb * L::LM + j) = pack_bf16(mr[2], mr[3]);
+      uint32_t ra[2], rb[2];
+      split_bf16<2>(mr[0], mr[1], ra);
+      split_bf16<2>(mr[2], mr[3], rb);
+      *reinterpret_cast<uint32_t*>(MR + ta * L::LM + j) = ra[0];
+      *reinterpret_cast<uint32_t*>(MR + tb * L::LM + j) = rb[0];
+      *reinterpret_cast<uint32_t*>(M2 + ta * L::LM + j) = ra[1];
+      *reinterpret_cast<uint32_t*>(M2 + tb * L::LM + j) = rb[1];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -354,12 +361,15 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (k <= rt) {
-        uint32_t af[4];
+        uint32_t af[4], cf[4];
         ldsm4(af, ar + 2 * frag_a(lane, 16 * rt, 16 * k, L::LM));
+        ldsm4(cf, a2 + 2 * frag_a(lane, 16 * rt, 16 * k, L::LM));
 #pragma unroll
         for (int m = 0; m < NH / 16; ++m) {
           uint32_t bf[4];
           ldsm4t(bf, ab + 2 * frag_bt(lane, n0 + 16 * m, 16 * k, L::LN));
+          mma_bf16(acc[2 * m], cf, bf[0], bf[1]);
+          mma_bf16(acc[2 * m + 1], cf, bf[2], bf[3]);
           mma_bf16(acc[2 * m], af, bf[0], bf[1]);
           mma_bf16(acc[2 * m + 1], af, bf[2], bf[3]);
         }
@@ -386,12 +396,15 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (k >= rt) {
-        uint32_t af[4];
+        uint32_t af[4], cf[4];
         ldsm4t(af, ar + 2 * frag_at(lane, 16 * rt, 16 * k, L::LM));
+        ldsm4t(cf, a2 + 2 * frag_at(lane, 16 * rt, 16 * k, L::LM));
 #pragma unroll
         for (int m = 0; m < NH / 16; ++m) {
           uint32_t bf[4];
           ldsm4t(bf, ac + 2 * frag_bt(lane, n0 + 16 * m, 16 * k, L::LN));
+          mma_bf16(acc[2 * m], cf, bf[0], bf[1]);
+          mma_bf16(acc[2 * m + 1], cf, bf[2], bf[3]);
           mma_bf16(acc[2 * m], af, bf[0], bf[1]);
           mma_bf16(acc[2 * m + 1], af, bf[2], bf[3]);
         }
