@@ -43,7 +43,7 @@ static SsmBwdWs ssm_bwd_ws(const sdm_ssm_dims* d, int Q, void* base) {
   w.gS = take(BH * nch * PN);
   w.ST = take(BH * PN);
   w.lg = take(BH * nch);
-  w.dAD = take(BH * nch * 2);
+  w.dAD = reinterpret_cast<double*>(take(BH * nch * 4));
   if (d->H != d->G) {
     w.pB = take(BH * d->T * d->d_k);
     w.pC = take(BH * d->T * d->d_k);
@@ -156,7 +156,8 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
   float* rowE = lo + Q;
   float* colE = rowE + Q;
   float* dg = colE + Q;      // R_tt
-  float* red = dg + Q;
+  // 8-byte aligned: an even number of floats lies before it
+  double* red = reinterpret_cast<double*>(dg + Q);
   const int c = blockIdx.x % a.nch, bh = blockIdx.x / a.nch;
   const int b = bh / a.H, h = bh - b * a.H, gr = h / a.hg;
   const int t0 = c * Q, n = min(Q, a.T - t0), tid = threadIdx.x;
@@ -171,9 +172,9 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
   load_rows(Cs, Np, Cm, a.sC, b, gr, t0, n, Q, N);
   __syncthreads();
   if (tid < 32) chunk_decay<1>(dts, A[h], hi, lo);
-  // <dSin, S_Q>
-  float bnd = 0.f;
-  for (size_t i = tid; i < PN; i += kBwdThreads) bnd = fmaf(dSin[i], Send[i], bnd);
+  // <dSin, S_Q>, in double: it enters every q of the chunk, and dA sums them over all steps
+  double bnd = 0.0;
+  for (size_t i = tid; i < PN; i += kBwdThreads) bnd = fma(double(dSin[i]), double(Send[i]), bnd);
   bnd = warp_sum(bnd);
   if ((tid & 31) == 0) red[tid >> 5] = bnd;
   __syncthreads();
@@ -322,19 +323,19 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
       ci += pc[tid * 33 + k];
       bi += pb[tid * 33 + k];
     }
-    const float yd = rowE[tid] + exp2f(hi[tid] + lo[tid]) * ci;
-    const float xu = colE[tid] + decay_between(hi[Q - 1], lo[Q - 1], hi[tid], lo[tid]) * bi;
-    float q = yd - dts[tid] * xu;
+    const double yd = double(rowE[tid]) + double(exp2f(hi[tid] + lo[tid])) * ci;
+    const double xu = double(colE[tid]) + double(decay_between(hi[Q - 1], lo[Q - 1], hi[tid], lo[tid])) * bi;
+    double q = yd - dts[tid] * xu;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {  // suffix sum
-      const float u = __shfl_down_sync(0xffffffffu, q, o);
+      const double u = __shfl_down_sync(0xffffffffu, q, o);
       if (tid + o < 32) q += u;
     }
-    float end = 0.f;
+    double end = 0.0;
     for (int k = 0; k < kBwdThreads / 32; ++k) end += red[k];
     q += end;
-    if (tid < n) ddt[row_off(ba.sddt, b, h, t0 + tid)] = fmaf(A[h], q, xu);
-    const float sA = warp_sum(dts[tid] * q), sD = warp_sum(tid < n ? dg[tid] : 0.f);
+    if (tid < n) ddt[row_off(ba.sddt, b, h, t0 + tid)] = float(A[h] * q + xu);
+    const double sA = warp_sum(double(dts[tid]) * q), sD = warp_sum(tid < n ? double(dg[tid]) : 0.0);
     if (tid == 0) {
       w.dAD[size_t(blockIdx.x) * 2] = sA;
       w.dAD[size_t(blockIdx.x) * 2 + 1] = sD;
@@ -369,14 +370,14 @@ k_ssm_fold(SsmBwdArgs ba, const float* __restrict__ pB, const float* __restrict_
 
 // dA, dD: a CTA per head sums its batches' and chunks' parts in a fixed order.
 __global__ void __launch_bounds__(256)
-k_ssm_dAD(const float* __restrict__ part, int B, int H, int nch, float* __restrict__ dA,
+k_ssm_dAD(const double* __restrict__ part, int B, int H, int nch, float* __restrict__ dA,
           float* __restrict__ dD) {
-  __shared__ float rA[8], rD[8];
+  __shared__ double rA[8], rD[8];
   const int h = blockIdx.x, n = B * nch;
-  float sA = 0.f, sD = 0.f;
+  double sA = 0.0, sD = 0.0;
   for (int i = threadIdx.x; i < n; i += 256) {
     const int b = i / nch, c = i - b * nch;
-    const float2 v = *reinterpret_cast<const float2*>(part + ((size_t(b) * H + h) * nch + c) * 2);
+    const double2 v = *reinterpret_cast<const double2*>(part + ((size_t(b) * H + h) * nch + c) * 2);
     sA += v.x;
     sD += v.y;
   }
@@ -392,8 +393,8 @@ k_ssm_dAD(const float* __restrict__ part, int B, int H, int nch, float* __restri
       sA += rA[k];
       sD += rD[k];
     }
-    dA[h] = sA;
-    if (dD) dD[h] = sD;
+    dA[h] = float(sA);
+    if (dD) dD[h] = float(sD);
   }
 }
 

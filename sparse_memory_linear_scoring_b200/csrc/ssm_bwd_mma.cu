@@ -139,7 +139,7 @@ struct SsmGradTile {
   static constexpr int elems = 2 * kGQ * (LX + LN) + 3 * SP + 3 * kGQ * LM;
   // decays [5][64], row sums of E and dots with C, B [2][3][64], column sums [4][64],
   // boundary [8], R_tt [64]
-  static constexpr int floats = 5 * kGQ + 6 * kGQ + 4 * kGQ + kGQ + 8;
+  static constexpr int floats = 5 * kGQ + 6 * kGQ + 4 * kGQ + kGQ + 2 * 8;
   static constexpr size_t smem = size_t(2) * elems + 4 * floats;
 };
 
@@ -187,7 +187,7 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
   float* dotB = dotC + 2 * kGQ;  // [2][64] B_j.I2_j
   float* colE = dotB + 2 * kGQ;  // [4][64]
   float* dg = colE + 4 * kGQ;    // [64] R_tt
-  float* red = dg + kGQ;         // [8]
+  double* red = reinterpret_cast<double*>(dg + kGQ);  // [8]
   const uint32_t ax = smem_u32(xs), ay = smem_u32(ys), ab = smem_u32(Bs), ac = smem_u32(Cs),
                  as = smem_u32(Ss), ag = smem_u32(MG), ar = smem_u32(MR), a2 = smem_u32(M2);
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5, g = lane >> 2, q = lane & 3;
@@ -378,12 +378,13 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
   }
   __syncthreads();  // everyone is done with S_0
   split_state<P, N>(Ss, dSin);
-  {  // <dSin, S_Q>
-    float s = 0.f;
+  {  // <dSin, S_Q>, in double: it enters every q of the chunk, and dA sums them over all steps
+    double s = 0.0;
 #pragma unroll 4
     for (int i = tid; i < int(PN) / 4; i += NT) {
       const float4 u = *reinterpret_cast<const float4*>(dSin + 4 * i), v = *reinterpret_cast<const float4*>(Send + 4 * i);
-      s = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, s))));
+      s = fma(double(u.x), double(v.x), fma(double(u.y), double(v.y), s));
+      s = fma(double(u.z), double(v.z), fma(double(u.w), double(v.w), s));
     }
     s = warp_sum(s);
     if (lane == 0) red[wp] = s;
@@ -464,39 +465,41 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
   }
   __syncthreads();
   if (wp == 0) {
-    float xu[2], v[2];
+    float xu[2];
+    double v[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
-      const float yd = rowE[t] + rowE[kGQ + t] + eg[t] * (dotC[t] + dotC[kGQ + t]);
-      float ce = 0.f;
+      const double yd = double(rowE[t]) + rowE[kGQ + t] + double(eg[t]) * (dotC[t] + dotC[kGQ + t]);
+      double ce = 0.0;
 #pragma unroll
       for (int r = 0; r < 4; ++r) ce += colE[r * kGQ + t];
-      xu[i] = ce + ej[t] * (dotB[t] + dotB[kGQ + t]);
-      v[i] = yd - dts[t] * xu[i];
+      ce += double(ej[t]) * (dotB[t] + dotB[kGQ + t]);
+      xu[i] = float(ce);
+      v[i] = yd - dts[t] * ce;
     }
-    float s = v[0] + v[1];
-    float suf = s;
+    const double s = v[0] + v[1];
+    double suf = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {  // suffix sum over the lanes
-      const float u = __shfl_down_sync(0xffffffffu, suf, o);
+      const double u = __shfl_down_sync(0xffffffffu, suf, o);
       if (lane + o < 32) suf += u;
     }
-    float end = 0.f;
+    double end = 0.0;
 #pragma unroll
     for (int k = 0; k < kGradWarps; ++k) end += red[k];
-    const float q1 = (suf - s) + v[1] + end, q0 = suf + end;
+    const double q1 = (suf - s) + v[1] + end, q0 = suf + end;
     const float Ah = A[h];
-    float sA = 0.f, sD = 0.f;
+    double sA = 0.0, sD = 0.0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
-      const float qt = i ? q1 : q0;
+      const double qt = i ? q1 : q0;
       if (t < n) {
-        ddt[row_off(ba.sddt, b, h, t0 + t)] = fmaf(Ah, qt, xu[i]);
+        ddt[row_off(ba.sddt, b, h, t0 + t)] = float(Ah * qt + xu[i]);
         sD += dg[t];
       }
-      sA = fmaf(dts[t], qt, sA);
+      sA = fma(double(dts[t]), qt, sA);
     }
     sA = warp_sum(sA);
     sD = warp_sum(sD);

@@ -93,7 +93,7 @@ struct SsmBwdWs {
   float* gS;    // [BH][nch][P][N] gradient arriving at each chunk's end
   float* ST;    // [BH][P][N] last state
   float* lg;    // [BH][nch] log2 decay of each chunk
-  float* dAD;   // [BH][nch][2] parts of dA and dD
+  double* dAD;  // [BH][nch][2] parts of dA and dD
   float* pB;    // [BH][T][N] per-head dB, dC where heads share them
   float* pC;
   size_t total;
