@@ -7,11 +7,14 @@
 // Both directions move bytes and little else, but not by much: 2K + 5 flops and two
 // special functions an element against 4 bytes in bf16, so a plain division (about 10
 // instructions) for the sigmoid would bound them.  A thread keeps the window of the
-// last K - 1 inputs of a few neighbouring channels -- 4 forward, 2 backward, where the
-// filter, its gradient and two windows share the registers -- and walks a tile of
-// steps with 8 rows of loads in flight; narrow threads leave room for enough warps to
-// cover the loads.  Every input is read once from DRAM, plus K - 1 rows a tile that
-// its neighbour has brought into L2.
+// last K - 1 inputs of 4 neighbouring channels (2 in the float32 backward, where the
+// filter, its gradient and two windows share the registers) and walks a tile of steps,
+// the next rows (8 forward, 4 backward) on their way while one group is computed, two
+// multiply-adds to an instruction.  Every input is read once from DRAM, plus K - 1 rows a
+// tile that its neighbour has brought into L2.  65536 steps of 1280 bf16 channels: forward
+// 70 us (336 MB, 4.8 TB/s), backward 143 us (503 MB, 3.5 TB/s; 25 instructions an element
+// at 4 CTAs of 128 threads an SM bound it); 16-byte threads without rows ahead and with
+// plain divisions took 208 and 660.
 #include "seq_internal.cuh"
 
 namespace sdm {

@@ -189,7 +189,7 @@ k_ssm_walk(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float eg = exp2f(hi[t + u] + lo[t + u]);
+          const float eg = ex2(hi[t + u] + lo[t + u]);
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[u][v] *= eg;
         }
@@ -216,7 +216,7 @@ k_ssm_walk(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
       }
       __syncthreads();
     }
-    const float eq = exp2f(gq);
+    const float eq = ex2(gq);
     for (int tile = tid; tile < np4 * nn4; tile += kWalkThreads) {
       const int p = (tile / nn4) * 4, e = (tile % nn4) * 4;
       float acc[4][4];

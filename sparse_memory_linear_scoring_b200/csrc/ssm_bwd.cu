@@ -93,7 +93,7 @@ k_ssm_local(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
     xs[i] = in ? to_f32(x[row_off(a.sx, b, h, t0 + t) + p]) * dts[t] *
                      decay_between(hi[Q - 1], lo[Q - 1], hi[t], lo[t])
                : 0.f;
-    ys[i] = in ? to_f32(dy[row_off(a.sy, b, h, t0 + t) + p]) * exp2f(hi[t] + lo[t]) : 0.f;
+    ys[i] = in ? to_f32(dy[row_off(a.sy, b, h, t0 + t) + p]) * ex2(hi[t] + lo[t]) : 0.f;
   }
   __syncthreads();
   const size_t o = size_t(blockIdx.x) * P * N;
@@ -242,7 +242,7 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
 #pragma unroll
       for (int v = 0; v < 4; ++v) s = fmaf(acc[u][v], dot[(t + u) * Np + e + v], s);
       (forC ? pc : pb)[(t + u) * 33 + (e >> 2)] = s;
-      const float f = forC ? exp2f(hi[t + u] + lo[t + u])
+      const float f = forC ? ex2(hi[t + u] + lo[t + u])
                            : dts[t + u] * decay_between(hi[Q - 1], lo[Q - 1], hi[t + u], lo[t + u]);
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[u][v] *= f;
@@ -323,7 +323,7 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
       ci += pc[tid * 33 + k];
       bi += pb[tid * 33 + k];
     }
-    const double yd = double(rowE[tid]) + double(exp2f(hi[tid] + lo[tid])) * ci;
+    const double yd = double(rowE[tid]) + double(ex2(hi[tid] + lo[tid])) * ci;
     const double xu = double(colE[tid]) + double(decay_between(hi[Q - 1], lo[Q - 1], hi[tid], lo[tid])) * bi;
     double q = yd - dts[tid] * xu;
 #pragma unroll

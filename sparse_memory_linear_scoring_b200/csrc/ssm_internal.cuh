@@ -62,7 +62,7 @@ __device__ __forceinline__ void chunk_decay(const float* dts, float A, float* hi
 
 // exp(g_t - g_j) of the pairs above.
 __device__ __forceinline__ float decay_between(float hi_t, float lo_t, float hi_j, float lo_j) {
-  return exp2f((hi_t - hi_j) + (lo_t - lo_j));
+  return ex2((hi_t - hi_j) + (lo_t - lo_j));  // below 2^-126: 0
 }
 
 // Launchers.  The states kernel writes, per (head, segment), the segment's own
