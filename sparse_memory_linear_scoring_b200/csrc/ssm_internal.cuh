@@ -78,6 +78,9 @@ cudaError_t launch_ssm_fwd_mma(const SsmArgs& a, const void* x, const float* dt,
                                const void* Bm, const void* Cm, const float* D, float* S,
                                const int32_t* lengths, void* y, float* segS, float* segG,
                                cudaStream_t s);
+// Each segment's own contribution and decay on tcgen05 (ssm_tc.cu), d_k = 128.
+cudaError_t launch_ssm_seg(const SsmArgs& a, const void* x, const float* dt, const float* A, const void* Bm,
+                           const int32_t* lengths, float* segS, float* segG, cudaStream_t s);
 inline bool ssm_tensor_sizes(const sdm_ssm_dims* d) {
   return d->in_dtype == SDM_DTYPE_BF16 && d->d_v >= 64 && d->d_k >= 64;
 }

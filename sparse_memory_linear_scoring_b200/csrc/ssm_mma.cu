@@ -299,7 +299,7 @@ static cudaError_t launch_tile(const SsmArgs& a, const void* x, const float* dt,
                                cudaStream_t s) {
   using bf = __nv_bfloat16;
   const unsigned grid = unsigned(a.B * a.H) * unsigned(a.P / 64) * unsigned(a.nseg);
-  const int s0 = int(SsmTile<N, false>::smem), s1 = int(SsmTile<N, true>::smem);
+  const int s1 = int(SsmTile<N, true>::smem);
   auto go = [&](auto kernel, int sm) -> cudaError_t {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (r != cudaSuccess) return r;
@@ -308,7 +308,9 @@ static cudaError_t launch_tile(const SsmArgs& a, const void* x, const float* dt,
     return cudaGetLastError();
   };
   if (a.nseg == 1) return go(k_ssm_tile<N, true, 3>, s1);
-  cudaError_t e = go(k_ssm_tile<N, false, 3>, s0);
+  cudaError_t e;
+  if constexpr (N == 128) e = launch_ssm_seg(a, x, dt, A, Bm, lengths, segS, segG, s);
+  else e = go(k_ssm_tile<N, false, 3>, int(SsmTile<N, false>::smem));
   if (e == cudaSuccess) e = launch_ssm_carry(segS, segG, S, S, a.B * a.H, a.nseg, a.P * N, s);
   return e == cudaSuccess ? go(k_ssm_tile<N, true, 2>, s1) : e;
 }
