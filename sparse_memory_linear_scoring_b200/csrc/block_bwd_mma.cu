@@ -450,7 +450,7 @@ k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* 
         x[z] = make_uint4(0u, 0u, 0u, 0u);
         kx[z] = make_uint2(0u, 0u);
         if (fz[z] != -1.f) {
-          const int at = place(y0 + z0 + z) * D;
+          const size_t at = (size_t)place(y0 + z0 + z) * D;
           x[z] = *reinterpret_cast<const uint4*>(part + at);
           if (kz[z] != 0.f) kx[z] = *reinterpret_cast<const uint2*>(kpart + at);
         }

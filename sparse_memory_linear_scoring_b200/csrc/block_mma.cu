@@ -15,7 +15,6 @@
 #include <cuda_fp16.h>
 
 #include "block_internal.cuh"
-#include "mma_dev.cuh"
 
 namespace sdm {
 

@@ -19,9 +19,11 @@
 // of several segments S only makes y, whose product takes it rounded to bf16: there two
 // parts do (2^-16 of a term beside 2^-9), a fifth fewer products at 128 x 128.  The last
 // state then comes from the carry.
-// 65536 steps of 8 heads of 128 x 128: 300 us the outputs, 178 the first walk.  Warp-level
-// products (0.83 a ns and SM at most) and the instructions around them bound both: the
-// weights' exponentials with denormal results alone were worth 47 us.
+// 65536 steps of 8 heads of 128 x 128: 300 us the outputs.  Warp-level products (about 0.4
+// of the 0.83 a ns and SM they reach) and the instructions around them bound it: the
+// weights' exponentials with denormal results alone were worth 47 us; factors of rows and
+// columns in place of most of the exponentials took 13 us more.  The first walk took 178 us
+// this way at d_k = 128, where ssm_tc.cu now takes it.
 #include "mma_dev.cuh"
 #include "ssm_internal.cuh"
 

@@ -8,9 +8,11 @@
 // the last to the first, so that w needs no decay of F, only a running sum.  Twelve products
 // of 128 x d_v x 16 a chunk go to one of two TMEM buffers, and the other is drained into
 // float32 registers meanwhile: sums over chunks there round to nearest, where hundreds of
-// accumulations in the tensor core would truncate one way.  What bounds a chunk is the
-// threads' work, the split (about 65 instructions for 8 elements) and the drain; the
-// products, three quarters of the warp-level walk's time, take a fifth.
+// accumulations in the tensor core would truncate one way.  65536 steps of 8 heads of
+// 128 x 128: 96 us (warp-level products: 178), 3200 cycles a chunk, of which the products
+// need about 770; the threads' split (65 instructions for 8 elements), the single
+// thread's 12 issues and the drain follow one another.  Loads two chunks ahead (101 us) or
+// 512 threads (103) do not help.
 #include "mma_dev.cuh"
 #include "ssm_internal.cuh"
 #include "tc_dev.cuh"
