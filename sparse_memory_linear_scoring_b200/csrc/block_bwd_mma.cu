@@ -404,11 +404,11 @@ k_blk_delta(BlkArgs a, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16*
 // forward's join a lane looks up every LN-th part; two rows' loads are in flight (four
 // take registers that more warps use better).
 template <int D>
-__global__ void __launch_bounds__(256, 5)
+__global__ void __launch_bounds__(128, 10)
 k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ dq,
          sdm_strides sdq, int kt) {
   constexpr int LN = D / 8;
-  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
+  const long long i = ((long long)blockIdx.x * 128 + threadIdx.x) / LN;
   const int ln = threadIdx.x % LN, c = ln * 8;
   const bool in = i < (long long)a.B * a.G * a.nq * a.R;
   const long long i0 = in ? i : 0, bt = i0 / a.R;
@@ -451,8 +451,8 @@ k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* 
         kx[z] = make_uint2(0u, 0u);
         if (fz[z] != -1.f) {
           const size_t at = (size_t)place(y0 + z0 + z) * D;
-          x[z] = *reinterpret_cast<const uint4*>(part + at);
-          if (kz[z] != 0.f) kx[z] = *reinterpret_cast<const uint2*>(kpart + at);
+          x[z] = __ldcs(reinterpret_cast<const uint4*>(part + at));
+          if (kz[z] != 0.f) kx[z] = __ldcs(reinterpret_cast<const uint2*>(kpart + at));
         }
       }
 #pragma unroll
@@ -609,7 +609,7 @@ static cudaError_t launch_grad(const sdm_block_dims* d, BlkArgs a, const void* q
     e = kt == 32 ? go(std::integral_constant<int, 32>()) : go(std::integral_constant<int, 64>());
     if (e != cudaSuccess) return e;
     const long long nr = (long long)a.B * a.H * a.nq * (D / 8);
-    k_blk_dq<D><<<unsigned((nr + 255) / 256), 256, 0, s>>>(a, w, idx, (bf*)dq, gv->q, kt);
+    k_blk_dq<D><<<unsigned((nr + 127) / 128), 128, 0, s>>>(a, w, idx, (bf*)dq, gv->q, kt);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_blk_dkv(a, w, true, dk, dv, gv->k, gv->v, kt, q0 == 0, q0 + a.nq == d->Tq, s);
     if (e != cudaSuccess) return e;

@@ -35,11 +35,11 @@ static int item_rows(const sdm_block_dims* d, int nq) {
 // (query, slot) pairs without keys have no partial and are skipped by the same test
 // that left them out.
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(64)
 k_blk_join(BlkArgs a, BlkFwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ o,
            float* __restrict__ lse) {
   constexpr int LN = D / 8;
-  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
+  const long long i = ((long long)blockIdx.x * 64 + threadIdx.x) / LN;
   const int ln = threadIdx.x % LN, c = ln * 8;
   const bool in = i < (long long)a.B * a.G * a.nq * a.R;
   const long long i0 = in ? i : 0;
@@ -77,7 +77,7 @@ k_blk_join(BlkArgs a, BlkFwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16
       for (int z = 0; z < 4; ++z) {
         fz[z] = __shfl_sync(0xffffffffu, f, z0 + z, LN);
         x[z] = make_uint4(0u, 0u, 0u, 0u);
-        if (fz[z] != -1.f) x[z] = *reinterpret_cast<const uint4*>(part + (size_t)(s0 + z0 + z) * a.R * D);
+        if (fz[z] != -1.f) x[z] = __ldcs(reinterpret_cast<const uint4*>(part + (size_t)(s0 + z0 + z) * a.R * D));
       }
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
@@ -154,7 +154,7 @@ static cudaError_t launch_fwd(const sdm_block_dims* d, BlkArgs a, const void* q,
     e = launch_blk_tc(a, w, unsigned(grid), q, k, v, s);
     if (e != cudaSuccess) return e;
     const long long n = (long long)a.B * a.H * a.nq * (D / 8);
-    k_blk_join<D><<<unsigned((n + 255) / 256), 256, 0, s>>>(a, w, idx, (bf*)o, lse);
+    k_blk_join<D><<<unsigned((n + 63) / 64), 64, 0, s>>>(a, w, idx, (bf*)o, lse);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return cudaSuccess;
