@@ -9,13 +9,13 @@
 //   O = P V (tcgen05.mma; V is MN-major as it lies, so nothing is transposed),
 //   O over the row's largest element as halves, through shared memory to the parts.
 // The products take a few percent of the time.  What bounds a tile is the softmax, the
-// conversion of O, the gather and the way out, about 1600 instructions a thread (13 a
-// row and lane, where warp-level fragments cost 65: four lanes shared each row's maxima
-// and sums, and every operand went through registers), and a chain of four waits: 3 CTAs
-// an SM (at d = 128, by shared memory) run side by side instead of one with more stages,
-// so the queries' place serves P and the outgoing rows, and S and O share TMEM columns.
-// 8192 tokens, 2 sequences, 16 heads of 128 on 4, 16 blocks of 64: 422 us, of which the
-// 1.1 GB of parts take 100; two threads a row (24 warps an SM for 12) took 486, a bulk
+// conversion of O, the gather and the way out, 47 warp instructions a row (warp-level
+// fragments, where four lanes share each row's maxima and sums and every operand goes
+// through registers, took 65), and a chain of four waits: 3 CTAs an SM (at d = 128, by
+// shared memory) run side by side instead of one with more stages, so the queries' place
+// serves P and the outgoing rows, and S and O share TMEM columns.
+// 8192 tokens, 2 sequences, 16 heads of 128 on 4, 16 blocks of 64: 397 us, of which the
+// 1.1 GB of parts take about 80; two threads a row (24 warps an SM for 12) took 486, a bulk
 // copy for each outgoing row 444, paired float32 instructions 465 (register moves).
 #include <cuda_fp16.h>
 
@@ -292,13 +292,21 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
     __syncwarp();
     // the warp's rows go out with consecutive lanes on consecutive pieces (a bulk copy a row
     // took 2200 cycles a tile, 64 a copy)
+    constexpr int NW = 4;  // pieces read together (one: 423 us at the case above, four 397, eight 423)
 #pragma unroll
-    for (int i = lane; i < 32 * (D / 8); i += 32) {
-      const int rr = i / (D / 8), c = i % (D / 8);
-      const size_t to = __shfl_sync(0xffffffffu, place, rr);
-      if (base + 32 * wp + rr < r1)
-        *reinterpret_cast<uint4*>(part + to * D + 8 * c) =
-            *reinterpret_cast<const uint4*>(work + (32 * wp + rr) * L::OP + 16 * c);
+    for (int i0 = 0; i0 < D / 8; i0 += NW) {
+      uint4 u[NW];
+#pragma unroll
+      for (int z = 0; z < NW; ++z) {
+        const int i = lane + 32 * (i0 + z), rr = i / (D / 8), c = i % (D / 8);
+        u[z] = *reinterpret_cast<const uint4*>(work + (32 * wp + rr) * L::OP + 16 * c);
+      }
+#pragma unroll
+      for (int z = 0; z < NW; ++z) {
+        const int i = lane + 32 * (i0 + z), rr = i / (D / 8), c = i % (D / 8);
+        const size_t to = __shfl_sync(0xffffffffu, place, rr);
+        if (base + 32 * wp + rr < r1) *reinterpret_cast<uint4*>(part + to * D + 8 * c) = u[z];
+      }
     }
     if (base + kTcRows < r1) {
       look(base + kTcRows + tid);
