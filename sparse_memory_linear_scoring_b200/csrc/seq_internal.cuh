@@ -103,6 +103,27 @@ __device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T) {
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
+// Kernels that follow one another closely are launched while the one before them ends
+// (programmatic stream serialization) and wait for it here, before they touch memory.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c;
+  memset(&c, 0, sizeof(c));
+  cudaLaunchAttribute at;
+  memset(&at, 0, sizeof(at));
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.gridDim = grid;
+  c.blockDim = dim3(unsigned(threads));
+  c.dynamicSmemBytes = size_t(smem);
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // 2^x on the special function unit; results below 2^-126 are 0.
 __device__ __forceinline__ float ex2(float x) {
   float r;

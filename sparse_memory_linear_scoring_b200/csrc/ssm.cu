@@ -27,6 +27,7 @@ struct Carry {
 
 __global__ void __launch_bounds__(128)
 k_ssm_carry(Carry c0, Carry c1, const float* __restrict__ segG, int nseg, int PN) {
+  wait_for_previous();
   const Carry c = blockIdx.z ? c1 : c0;
   const int bh = blockIdx.y;
   const int e = (blockIdx.x * 128 + threadIdx.x) * 4;
@@ -69,7 +70,7 @@ static cudaError_t launch_carry(const Carry& c0, const Carry& c1, int both, cons
     auto at = [&](const Carry& c) {
       return Carry{c.segS + o * nseg, c.S0 ? c.S0 + o : nullptr, c.S_end ? c.S_end + o : nullptr, c.reverse};
     };
-    k_ssm_carry<<<dim3((PN / 4 + 127) / 128, n, both ? 2 : 1), 128, 0, s>>>(
+    launch_after(k_ssm_carry, dim3((PN / 4 + 127) / 128, n, both ? 2 : 1), 128, 0, s,
         at(c0), at(c1), segG + size_t(b0) * nseg, nseg, PN);
   }
   return cudaGetLastError();
@@ -104,6 +105,7 @@ k_ssm_walk(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
            const float* __restrict__ A, const Tin* __restrict__ Bm, const Tin* __restrict__ Cm,
            const float* __restrict__ D, float* __restrict__ S, const int32_t* __restrict__ lengths,
            Tin* __restrict__ y, float* __restrict__ segS, float* __restrict__ segG) {
+  wait_for_previous();
   extern __shared__ __align__(16) float sm[];
   constexpr int Q = kSsmQ;
   const int P = a.P, N = a.N, Np = N + 1, Qp = Q + 1;
@@ -264,6 +266,7 @@ __global__ void __launch_bounds__(kStepThreads)
 k_ssm_step(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
            const float* __restrict__ A, const Tin* __restrict__ Bm, const Tin* __restrict__ Cm,
            const float* __restrict__ D, float* __restrict__ S, Tin* __restrict__ y, int tiles) {
+  wait_for_previous();
   const int bh = blockIdx.x / tiles, tile = blockIdx.x - bh * tiles;
   const int b = bh / a.H, h = bh - b * a.H, gr = h / a.hg;
   const int ln = a.N >> 2;  // lanes per row (4..32)
@@ -374,7 +377,7 @@ static cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, const void* x, const fl
     if ((e = cudaFuncSetAttribute(k_ssm_walk<Tin, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   smem)) != cudaSuccess)
       return e;
-    k_ssm_walk<Tin, false><<<grid, kWalkThreads, smem, s>>>(
+    launch_after(k_ssm_walk<Tin, false>, grid, kWalkThreads, smem, s,
         a, (const Tin*)x, dt, A, (const Tin*)Bm, (const Tin*)Cm, D, S, lengths, (Tin*)y, segS, segG);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_ssm_carry(segS, segG, S, nullptr, a.B * a.H, a.nseg, a.P * a.N, s)) !=
@@ -384,7 +387,7 @@ static cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, const void* x, const fl
   if ((e = cudaFuncSetAttribute(k_ssm_walk<Tin, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 smem)) != cudaSuccess)
     return e;
-  k_ssm_walk<Tin, true><<<grid, kWalkThreads, smem, s>>>(
+  launch_after(k_ssm_walk<Tin, true>, grid, kWalkThreads, smem, s,
       a, (const Tin*)x, dt, A, (const Tin*)Bm, (const Tin*)Cm, D, S, lengths, (Tin*)y, segS, segG);
   return cudaGetLastError();
 }
@@ -468,11 +471,11 @@ extern "C" int sdm_ssm_step(const void* x, const float* dt, const float* A, cons
   const unsigned grid = unsigned(a.B * a.H) * unsigned(tiles);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dims->in_dtype == SDM_DTYPE_BF16)
-    k_ssm_step<__nv_bfloat16><<<grid, kStepThreads, 0, s>>>(
+    launch_after(k_ssm_step<__nv_bfloat16>, grid, kStepThreads, 0, s,
         a, (const __nv_bfloat16*)x, dt, A, (const __nv_bfloat16*)Bm, (const __nv_bfloat16*)Cm, D,
         S_inout, (__nv_bfloat16*)y, tiles);
   else
-    k_ssm_step<float><<<grid, kStepThreads, 0, s>>>(a, (const float*)x, dt, A, (const float*)Bm,
+    launch_after(k_ssm_step<float>, grid, kStepThreads, 0, s, a, (const float*)x, dt, A, (const float*)Bm,
                                                     (const float*)Cm, D, S_inout, (float*)y, tiles);
   return cudaGetLastError() == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }

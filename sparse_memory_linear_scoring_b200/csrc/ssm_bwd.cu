@@ -68,6 +68,7 @@ k_ssm_local(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
             const float* __restrict__ A, const Tin* __restrict__ Bm, const Tin* __restrict__ Cm,
             const Tin* __restrict__ dy, float* __restrict__ fS, float* __restrict__ gS,
             float* __restrict__ lg) {
+  wait_for_previous();
   extern __shared__ __align__(16) float sm[];
   constexpr int Q = kSsmQ;
   const int P = a.P, N = a.N;
@@ -137,6 +138,7 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
           const float* __restrict__ A, const Tin* __restrict__ Bm, const Tin* __restrict__ Cm,
           const float* __restrict__ D, const Tin* __restrict__ dy, SsmBwdWs w, Tin* __restrict__ dx,
           float* __restrict__ ddt, Tin* __restrict__ dB, Tin* __restrict__ dC) {
+  wait_for_previous();
   extern __shared__ __align__(16) float sm[];
   const SsmArgs& a = ba.a;
   constexpr int Q = kSsmQ, Qp = Q + 1;
@@ -348,6 +350,7 @@ template <typename Tin>
 __global__ void __launch_bounds__(256)
 k_ssm_fold(SsmBwdArgs ba, const float* __restrict__ pB, const float* __restrict__ pC,
            Tin* __restrict__ dB, Tin* __restrict__ dC) {
+  wait_for_previous();
   const SsmArgs& a = ba.a;
   const int nn4 = a.N >> 2;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -372,6 +375,7 @@ k_ssm_fold(SsmBwdArgs ba, const float* __restrict__ pB, const float* __restrict_
 __global__ void __launch_bounds__(256)
 k_ssm_dAD(const double* __restrict__ part, int B, int H, int nch, float* __restrict__ dA,
           float* __restrict__ dD) {
+  wait_for_previous();
   __shared__ double rA[8], rD[8];
   const int h = blockIdx.x, n = B * nch;
   double sA = 0.0, sD = 0.0;
@@ -412,12 +416,12 @@ static cudaError_t launch_ssm_bwd_simt(const SsmBwdArgs& ba, const void* x, cons
   if ((e = cudaFuncSetAttribute(k_ssm_local<Tin>, cudaFuncAttributeMaxDynamicSharedMemorySize, s1)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(k_ssm_bwd<Tin>, cudaFuncAttributeMaxDynamicSharedMemorySize, s2)) != cudaSuccess)
     return e;
-  k_ssm_local<Tin><<<grid, kBwdThreads, s1, s>>>(a, (const Tin*)x, dt, A, (const Tin*)Bm,
+  launch_after(k_ssm_local<Tin>, grid, kBwdThreads, s1, s, a, (const Tin*)x, dt, A, (const Tin*)Bm,
                                                  (const Tin*)Cm, (const Tin*)dy, w.fS, w.gS, w.lg);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int BH = a.B * a.H, PN = a.P * a.N;
   if ((e = launch_ssm_carries(w.fS, w.gS, w.lg, S0, w.ST, dST, dS0, BH, a.nch, PN, s)) != cudaSuccess) return e;
-  k_ssm_bwd<Tin><<<grid, kBwdThreads, s2, s>>>(ba, (const Tin*)x, dt, A, (const Tin*)Bm,
+  launch_after(k_ssm_bwd<Tin>, grid, kBwdThreads, s2, s, ba, (const Tin*)x, dt, A, (const Tin*)Bm,
                                                (const Tin*)Cm, D, (const Tin*)dy, w, (Tin*)dx, ddt,
                                                (Tin*)dB, (Tin*)dC);
   return cudaGetLastError();
@@ -429,7 +433,7 @@ static cudaError_t launch_ssm_fold(const SsmBwdArgs& ba, const SsmBwdWs& w, void
   const SsmArgs& a = ba.a;
   if (a.hg == 1) return cudaSuccess;
   const long long n = (long long)a.B * a.G * a.T * (a.N / 4);
-  k_ssm_fold<Tin><<<dim3(unsigned((n + 255) / 256), 2), 256, 0, s>>>(ba, w.pB, w.pC, (Tin*)dB, (Tin*)dC);
+  launch_after(k_ssm_fold<Tin>, dim3(unsigned((n + 255) / 256), 2), 256, 0, s, ba, w.pB, w.pC, (Tin*)dB, (Tin*)dC);
   return cudaGetLastError();
 }
 
@@ -486,7 +490,7 @@ extern "C" int sdm_ssm_backward(const void* x, const float* dt, const float* A, 
   if (e == cudaSuccess)
     e = bf ? launch_ssm_fold<__nv_bfloat16>(ba, w, dB, dC, s) : launch_ssm_fold<float>(ba, w, dB, dC, s);
   if (e == cudaSuccess) {
-    k_ssm_dAD<<<dims->H, 256, 0, s>>>(w.dAD, dims->B, dims->H, ba.a.nch, dA, dD);
+    launch_after(k_ssm_dAD, dims->H, 256, 0, s, w.dAD, dims->B, dims->H, ba.a.nch, dA, dD);
     e = cudaGetLastError();
   }
   return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;

@@ -64,6 +64,7 @@ k_ssm_local_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __
                  const float* __restrict__ A, const __nv_bfloat16* __restrict__ Bm,
                  const __nv_bfloat16* __restrict__ Cm, const __nv_bfloat16* __restrict__ dy,
                  float* __restrict__ fS, float* __restrict__ gS, float* __restrict__ lg) {
+  wait_for_previous();
   using L = LocalTile<P, N>;
   extern __shared__ __align__(16) unsigned char raw[];
   __nv_bfloat16* t_ = reinterpret_cast<__nv_bfloat16*>(raw);
@@ -169,6 +170,7 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
            const __nv_bfloat16* __restrict__ Cm, const float* __restrict__ D,
            const __nv_bfloat16* __restrict__ dy, SsmBwdWs w, __nv_bfloat16* __restrict__ dx,
            float* __restrict__ ddt, __nv_bfloat16* __restrict__ dB, __nv_bfloat16* __restrict__ dC) {
+  wait_for_previous();
   using L = SsmGradTile<P, N>;
   constexpr int NT = kGradWarps * 32;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -524,12 +526,12 @@ static cudaError_t launch_grad(const SsmBwdArgs& ba, const void* x, const float*
   if ((e = cudaFuncSetAttribute(k_ssm_local_tile<P, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, s1)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(k_ssm_grad<P, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, s2)) != cudaSuccess)
     return e;
-  k_ssm_local_tile<P, N><<<grid, 2 * P, s1, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm,
+  launch_after(k_ssm_local_tile<P, N>, grid, 2 * P, s1, s, a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm,
                                                 (const bf*)dy, w.fS, w.gS, w.lg);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_ssm_carries(w.fS, w.gS, w.lg, S0, w.ST, dST, dS0, a.B * a.H, a.nch, P * N, s)) != cudaSuccess)
     return e;
-  k_ssm_grad<P, N><<<grid, kGradWarps * 32, s2, s>>>(ba, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm,
+  launch_after(k_ssm_grad<P, N>, grid, kGradWarps * 32, s2, s, ba, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm,
                                                     D, (const bf*)dy, w, (bf*)dx, ddt, (bf*)dB, (bf*)dC);
   return cudaGetLastError();
 }

@@ -66,6 +66,7 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
            const __nv_bfloat16* __restrict__ Cm, const float* __restrict__ D, float* __restrict__ S,
            const int32_t* __restrict__ lengths, __nv_bfloat16* __restrict__ y,
            float* __restrict__ segS, float* __restrict__ segG) {
+  wait_for_previous();
   using L = SsmTile<N, OUT>;
   constexpr int P = L::P;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -305,7 +306,7 @@ static cudaError_t launch_tile(const SsmArgs& a, const void* x, const float* dt,
   auto go = [&](auto kernel, int sm) -> cudaError_t {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (r != cudaSuccess) return r;
-    kernel<<<grid, 128, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm, D, S, lengths, (bf*)y,
+    launch_after(kernel, grid, 128, sm, s, a, (const bf*)x, dt, A, (const bf*)Bm, (const bf*)Cm, D, S, lengths, (bf*)y,
                                  segS, segG);
     return cudaGetLastError();
   };

@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(kSegThreads)
 k_ssm_seg(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restrict__ dt,
           const float* __restrict__ A, const __nv_bfloat16* __restrict__ Bm,
           const int32_t* __restrict__ lengths, float* __restrict__ segS, float* __restrict__ segG) {
+  wait_for_previous();
   using L = SegTile<P>;
   constexpr int N = 128, Q = kSsmQT;
   extern __shared__ unsigned char raw0[];
@@ -208,7 +209,7 @@ cudaError_t launch_ssm_seg(const SsmArgs& a, const void* x, const float* dt, con
   auto go = [&](auto kernel, int sm) -> cudaError_t {
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (r != cudaSuccess) return r;
-    kernel<<<grid, kSegThreads, sm, s>>>(a, (const bf*)x, dt, A, (const bf*)Bm, lengths, segS, segG);
+    launch_after(kernel, grid, kSegThreads, sm, s, a, (const bf*)x, dt, A, (const bf*)Bm, lengths, segS, segG);
     return cudaGetLastError();
   };
   return a.P == 64 ? go(k_ssm_seg<64>, int(SegTile<64>::smem)) : go(k_ssm_seg<128>, int(SegTile<128>::smem));
