@@ -77,6 +77,7 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
           const int32_t* __restrict__ idx, Tin* __restrict__ o, float* __restrict__ lse,
           const Tin* __restrict__ d_o, float* __restrict__ delta, Tin* __restrict__ dq,
           sdm_strides sdo, sdm_strides sdq, int hc, int cs, int vec) {
+  wait_for_previous();
   constexpr int V = 16 / int(sizeof(Tin)), LN = D / V, KP = 32 / LN;
   constexpr int NB = LN < 8 ? LN : 8, NG = LN / NB;  // rows loaded together, such groups
   __shared__ float part[kRowWarps][RH][D];
@@ -308,16 +309,18 @@ static cudaError_t launch_row(const BlkArgs& a, const void* q, const void* k, co
   if (view_aligned(v, a.sv, es, 16)) vec |= 8;
   cudaLaunchConfig_t c;
   memset(&c, 0, sizeof(c));
-  cudaLaunchAttribute at;
-  memset(&at, 0, sizeof(at));
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = unsigned(cs);
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  memset(at, 0, sizeof(at));
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(cs);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_after()
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   c.gridDim = dim3(unsigned(items * cs));
   c.blockDim = dim3(kRowWarps * 32);
   c.stream = s;
-  c.attrs = &at;
-  c.numAttrs = 1;
+  c.attrs = at;
+  c.numAttrs = 2;
   return cudaLaunchKernelEx(&c, k_blk_row<Tin, D, RH, BWD>, a, (const Tin*)q, (const Tin*)k,
                             (const Tin*)v, idx, (Tin*)o, lse, (const Tin*)d_o, delta, (Tin*)dq, sdo,
                             sdq, hc, cs, vec);

@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(kKvThreads)
 k_blk_kv(BlkArgs a, BlkPlan pl, const Tin* __restrict__ q, const Tin* __restrict__ k,
          const Tin* __restrict__ v, const float* __restrict__ lse, const Tin* __restrict__ d_o,
          const float* __restrict__ delta, float* __restrict__ part, sdm_strides sdo, int vec) {
+  wait_for_previous();
   extern __shared__ __align__(16) float sm[];
   constexpr int Dp = D + 4;
   float* Ks = sm;
@@ -173,7 +174,7 @@ static cudaError_t launch_kv(const BlkArgs& a, const BlkPlan& pl, const void* q,
     constexpr int D = decltype(dd)::value;
     cudaError_t e = cudaFuncSetAttribute(k_blk_kv<Tin, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    k_blk_kv<Tin, D><<<unsigned(grid), kKvThreads, smem, s>>>(
+    launch_after(k_blk_kv<Tin, D>, unsigned(grid), kKvThreads, smem, s,
         a, pl, (const Tin*)q, (const Tin*)k, (const Tin*)v, lse, (const Tin*)d_o, delta, part, sdo, vec);
     return cudaGetLastError();
   };

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kGradThreads)
 k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
            const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
            const float* __restrict__ lse, const __nv_bfloat16* __restrict__ d_o, sdm_strides sdo) {
+  wait_for_previous();
   using L = GradTile<D, KT>;
   extern __shared__ __align__(16) unsigned char raw[];
   __nv_bfloat16* Ks = reinterpret_cast<__nv_bfloat16*>(raw);
@@ -382,6 +383,7 @@ template <int D>
 __global__ void __launch_bounds__(256)
 k_blk_delta(BlkArgs a, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ d_o,
             sdm_strides sdo, float* __restrict__ delta) {
+  wait_for_previous();
   constexpr int LN = D / 8;
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
   const int c = (threadIdx.x % LN) * 8;
@@ -407,6 +409,7 @@ template <int D>
 __global__ void __launch_bounds__(128, 10)
 k_blk_dq(BlkArgs a, BlkBwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ dq,
          sdm_strides sdq, int kt) {
+  wait_for_previous();
   constexpr int LN = D / 8;
   const long long i = ((long long)blockIdx.x * 128 + threadIdx.x) / LN;
   const int ln = threadIdx.x % LN, c = ln * 8;
@@ -479,6 +482,7 @@ template <typename Tin, int D>
 __global__ void __launch_bounds__(256)
 k_blk_dkv(BlkArgs a, BlkBwdWs w, Tin* __restrict__ dk, Tin* __restrict__ dv,
           sdm_strides sdk, sdm_strides sdv, int kt, int begin, int end, int vec) {
+  wait_for_previous();
   constexpr int LN = D / 4;
   long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const int c = int(i % LN) * 4;
@@ -524,10 +528,10 @@ cudaError_t launch_blk_dkv(const BlkArgs& a, const BlkBwdWs& w, bool bf16, void*
   auto go = [&](auto dd) {
     constexpr int D = decltype(dd)::value;
     if (bf16)
-      k_blk_dkv<__nv_bfloat16, D><<<grid, 256, 0, s>>>(a, w, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, sdk, sdv,
+      launch_after(k_blk_dkv<__nv_bfloat16, D>, grid, 256, 0, s, a, w, (__nv_bfloat16*)dk, (__nv_bfloat16*)dv, sdk, sdv,
                                                        kt, begin, end, vec);
     else
-      k_blk_dkv<float, D><<<grid, 256, 0, s>>>(a, w, (float*)dk, (float*)dv, sdk, sdv, kt, begin, end, vec);
+      launch_after(k_blk_dkv<float, D>, grid, 256, 0, s, a, w, (float*)dk, (float*)dv, sdk, sdv, kt, begin, end, vec);
     return cudaGetLastError();
   };
   return a.d == 32 ? go(std::integral_constant<int, 32>())
@@ -591,7 +595,7 @@ static cudaError_t launch_grad(const sdm_block_dims* d, BlkArgs a, const void* q
     const BlkBwdWs w = blk_bwd_ws(d, a.nq, workspace);
     if (q0 == 0) {
       const long long n = (long long)a.B * a.H * a.Tq * (D / 8);
-      k_blk_delta<D><<<unsigned((n + 255) / 256), 256, 0, s>>>(a, (const bf*)o, (const bf*)d_o, gv->o, w.delta);
+      launch_after(k_blk_delta<D>, unsigned((n + 255) / 256), 256, 0, s, a, (const bf*)o, (const bf*)d_o, gv->o, w.delta);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if ((e = launch_blk_plan(a, w.plan, idx, s)) != cudaSuccess) return e;
@@ -602,14 +606,14 @@ static cudaError_t launch_grad(const sdm_block_dims* d, BlkArgs a, const void* q
       const int sm = int(GradTile<D, KT>::smem);
       cudaError_t r = cudaFuncSetAttribute(k_blk_grad<D, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
       if (r != cudaSuccess) return r;
-      k_blk_grad<D, KT><<<unsigned(grid), kGradThreads, sm, s>>>(a, w, (const bf*)q, (const bf*)k,
+      launch_after(k_blk_grad<D, KT>, unsigned(grid), kGradThreads, sm, s, a, w, (const bf*)q, (const bf*)k,
                                                                  (const bf*)v, lse, (const bf*)d_o, gv->o);
       return cudaGetLastError();
     };
     e = kt == 32 ? go(std::integral_constant<int, 32>()) : go(std::integral_constant<int, 64>());
     if (e != cudaSuccess) return e;
     const long long nr = (long long)a.B * a.H * a.nq * (D / 8);
-    k_blk_dq<D><<<unsigned((nr + 127) / 128), 128, 0, s>>>(a, w, idx, (bf*)dq, gv->q, kt);
+    launch_after(k_blk_dq<D>, unsigned((nr + 127) / 128), 128, 0, s, a, w, idx, (bf*)dq, gv->q, kt);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_blk_dkv(a, w, true, dk, dv, gv->k, gv->v, kt, q0 == 0, q0 + a.nq == d->Tq, s);
     if (e != cudaSuccess) return e;

@@ -38,6 +38,7 @@ template <int D>
 __global__ void __launch_bounds__(64)
 k_blk_join(BlkArgs a, BlkFwdWs w, const int32_t* __restrict__ idx, __nv_bfloat16* __restrict__ o,
            float* __restrict__ lse) {
+  wait_for_previous();
   constexpr int LN = D / 8;
   const long long i = ((long long)blockIdx.x * 64 + threadIdx.x) / LN;
   const int ln = threadIdx.x % LN, c = ln * 8;
@@ -154,7 +155,7 @@ static cudaError_t launch_fwd(const sdm_block_dims* d, BlkArgs a, const void* q,
     e = launch_blk_tc(a, w, unsigned(grid), q, k, v, s);
     if (e != cudaSuccess) return e;
     const long long n = (long long)a.B * a.H * a.nq * (D / 8);
-    k_blk_join<D><<<unsigned((n + 63) / 64), 64, 0, s>>>(a, w, idx, (bf*)o, lse);
+    launch_after(k_blk_join<D>, unsigned((n + 63) / 64), 64, 0, s, a, w, idx, (bf*)o, lse);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -20,6 +20,7 @@ template <typename Tin>
 __global__ void __launch_bounds__(128)
 k_blk_pool(BlkArgs a, sdm_strides skc, const Tin* __restrict__ k, Tin* __restrict__ kc, int first,
            int count, int vec) {
+  wait_for_previous();
   __shared__ double red[128][4];
   const int bg = blockIdx.x / count, j = first + blockIdx.x - bg * count;
   const int b = bg / a.G, g = bg - b * a.G;
@@ -143,6 +144,7 @@ template <typename Tin, bool ONE>
 __global__ void __launch_bounds__(kSelThreads)
 k_blk_select(BlkArgs a, sdm_strides skc, const Tin* __restrict__ q, const Tin* __restrict__ kc,
              int nkc, int32_t* __restrict__ idx, int vec) {
+  wait_for_previous();
   extern __shared__ __align__(16) double sd[];
   const int d = a.d, dp = d + 2, m = a.n_sel - 1;  // pitch: 16-byte reads of 8 rows without conflicts
   double* qs = sd;
@@ -303,6 +305,7 @@ k_blk_select(BlkArgs a, sdm_strides skc, const Tin* __restrict__ q, const Tin* _
 // shares in order, so the lists come out in query order whatever runs first.
 __global__ void __launch_bounds__(256)
 k_blk_count(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
+  wait_for_previous();
   extern __shared__ int cnt[];
   const int sg = blockIdx.x % p.nseg, bg = blockIdx.x / p.nseg;
   for (int j = threadIdx.x; j < a.nb; j += 256) cnt[j] = 0;
@@ -321,6 +324,7 @@ k_blk_count(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx) {
 
 __global__ void __launch_bounds__(1024)
 k_blk_offsets(BlkArgs a, BlkPlan p) {
+  wait_for_previous();
   __shared__ int2 wsum[32];
   const int bg = blockIdx.x, tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   int* hist = p.hist + (size_t)bg * p.nseg * a.nb;
@@ -377,6 +381,7 @@ k_blk_offsets(BlkArgs a, BlkPlan p) {
 // first positions warp by warp, and each places its part.
 __global__ void __launch_bounds__(256)
 k_blk_place(BlkArgs a, BlkPlan p, const int32_t* __restrict__ idx, int W) {
+  wait_for_previous();
   extern __shared__ int at[];  // [W][nb]
   const int sg = blockIdx.x % p.nseg, bg = blockIdx.x / p.nseg;
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, nt = 32 * W;
@@ -464,9 +469,9 @@ cudaError_t launch_blk_plan(const BlkArgs& a, const BlkPlan& p, const int32_t* i
       (e = cudaFuncSetAttribute(k_blk_place, cudaFuncAttributeMaxDynamicSharedMemorySize, W * smem)) != cudaSuccess)
     return e;
   const unsigned grid = unsigned(a.B * a.G) * unsigned(p.nseg);
-  k_blk_count<<<grid, 256, smem, s>>>(a, p, idx);
-  k_blk_offsets<<<a.B * a.G, 1024, 0, s>>>(a, p);
-  k_blk_place<<<grid, 32 * W, W * smem, s>>>(a, p, idx, W);
+  launch_after(k_blk_count, grid, 256, smem, s, a, p, idx);
+  launch_after(k_blk_offsets, a.B * a.G, 1024, 0, s, a, p);
+  launch_after(k_blk_place, grid, 32 * W, W * smem, s, a, p, idx, W);
   return cudaGetLastError();
 }
 
@@ -530,10 +535,10 @@ extern "C" int sdm_block_pool(const void* k, void* kc, int32_t first, const sdm_
   const int vec = view_aligned(k, a.sk, int(es), 4 * es);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dims->in_dtype == SDM_DTYPE_BF16)
-    k_blk_pool<__nv_bfloat16><<<unsigned(grid), 128, 0, s>>>(a, views->kc, (const __nv_bfloat16*)k,
+    launch_after(k_blk_pool<__nv_bfloat16>, unsigned(grid), 128, 0, s, a, views->kc, (const __nv_bfloat16*)k,
                                                              (__nv_bfloat16*)kc, first, n - first, vec);
   else
-    k_blk_pool<float><<<unsigned(grid), 128, 0, s>>>(a, views->kc, (const float*)k, (float*)kc,
+    launch_after(k_blk_pool<float>, unsigned(grid), 128, 0, s, a, views->kc, (const float*)k, (float*)kc,
                                                      first, n - first, vec);
   return cudaGetLastError() == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
@@ -547,7 +552,7 @@ static cudaError_t launch_select(const BlkArgs& a, const sdm_strides& skc, const
   auto go = [&](auto kernel) -> cudaError_t {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kSelThreads, smem, s>>>(a, skc, (const Tin*)q, (const Tin*)kc, nkc, idx, vec);
+    launch_after(kernel, grid, kSelThreads, smem, s, a, skc, (const Tin*)q, (const Tin*)kc, nkc, idx, vec);
     return cudaGetLastError();
   };
   return a.Tq == 1 ? go(k_blk_select<Tin, true>) : go(k_blk_select<Tin, false>);

@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kStepWarps * 32)
 k_blk_step(BlkArgs a, const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
            const __nv_bfloat16* __restrict__ v, const int32_t* __restrict__ idx,
            __nv_bfloat16* __restrict__ o, float* __restrict__ lse, int hc, int cs) {
+  wait_for_previous();
   using L = StepTile<D>;
   extern __shared__ __align__(16) unsigned char raw[];
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
@@ -236,17 +237,19 @@ static cudaError_t launch_step(const BlkArgs& a, const void* q, const void* k, c
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c;
   memset(&c, 0, sizeof(c));
-  cudaLaunchAttribute at;
-  memset(&at, 0, sizeof(at));
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = unsigned(cs);
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  memset(at, 0, sizeof(at));
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(cs);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_after()
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   c.gridDim = dim3(unsigned(items * cs));
   c.blockDim = dim3(kStepWarps * 32);
   c.dynamicSmemBytes = size_t(sm);
   c.stream = s;
-  c.attrs = &at;
-  c.numAttrs = 1;
+  c.attrs = at;
+  c.numAttrs = 2;
   return cudaLaunchKernelEx(&c, k_blk_step<D>, a, (const bf*)q, (const bf*)k, (const bf*)v, idx, (bf*)o, lse,
                             hc, cs);
 }

@@ -69,6 +69,7 @@ template <int D, int BS>
 __global__ void __launch_bounds__(kTcRows, D == 128 ? (BS == 128 ? 2 : 3) : (BS == 128 ? 3 : 4))
 k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
          const __nv_bfloat16* __restrict__ v) {
+  wait_for_previous();
   using L = TcTile<D, BS>;
   extern __shared__ unsigned char raw0[];
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
@@ -334,7 +335,7 @@ static cudaError_t launch_tc(const BlkArgs& a, const BlkFwdWs& w, unsigned grid,
   const int sm = int(TcTile<D, BS>::smem);
   const cudaError_t e = cudaFuncSetAttribute(k_blk_tc<D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
   if (e != cudaSuccess) return e;
-  k_blk_tc<D, BS><<<grid, kTcRows, sm, s>>>(a, w, (const bf*)q, (const bf*)k, (const bf*)v);
+  launch_after(k_blk_tc<D, BS>, grid, kTcRows, sm, s, a, w, (const bf*)q, (const bf*)k, (const bf*)v);
   return cudaGetLastError();
 }
 

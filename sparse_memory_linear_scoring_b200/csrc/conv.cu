@@ -97,6 +97,7 @@ template <typename T, int V, int K, bool SILU>
 __global__ void __launch_bounds__(128)
 k_conv_fwd(ConvArgs a, const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias,
            T* state, const int32_t* __restrict__ lengths, T* __restrict__ y) {
+  wait_for_previous();
   const int nv = a.d / V;
   long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long per_b = (long long)a.ntile * a.H * nv;
@@ -209,6 +210,7 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
            const T* __restrict__ bias, const T* __restrict__ state0, const T* __restrict__ dy,
            const float* __restrict__ dstate, T* __restrict__ dx, float* __restrict__ dstate0,
            float* __restrict__ part) {
+  wait_for_previous();
   __shared__ float red[kConvSub][32][V];
   const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
   const int nv = a.d / V;
@@ -371,6 +373,7 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
 __global__ void __launch_bounds__(256)
 k_conv_reduce(const float* __restrict__ part, int rows, int K, int C, float* __restrict__ dw,
               float* __restrict__ db) {
+  wait_for_previous();
   __shared__ float red[8][32];
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane, k = blockIdx.y;
@@ -416,10 +419,10 @@ static cudaError_t launch_conv_fwd(const ConvArgs& a, bool silu, const void* x, 
   const long long n = (long long)a.B * a.ntile * a.H * (a.d / V);
   const unsigned grid = unsigned((n + 127) / 128);
   if (silu)
-    k_conv_fwd<T, V, K, true><<<grid, 128, 0, s>>>(a, (const T*)x, (const T*)w, (const T*)bias,
+    launch_after(k_conv_fwd<T, V, K, true>, grid, 128, 0, s, a, (const T*)x, (const T*)w, (const T*)bias,
                                                    (T*)state, lengths, (T*)y);
   else
-    k_conv_fwd<T, V, K, false><<<grid, 128, 0, s>>>(a, (const T*)x, (const T*)w, (const T*)bias,
+    launch_after(k_conv_fwd<T, V, K, false>, grid, 128, 0, s, a, (const T*)x, (const T*)w, (const T*)bias,
                                                     (T*)state, lengths, (T*)y);
   return cudaGetLastError();
 }
@@ -431,16 +434,16 @@ static cudaError_t launch_conv_bwd(const ConvBwdArgs& a, bool silu, const void* 
                                    float* dstate0, float* part, cudaStream_t s) {
   const dim3 grid((a.H * (a.d / V) + 31) / 32, a.B * a.ntile);
   if (silu)
-    k_conv_bwd<T, V, K, true><<<grid, 32 * kConvSub, 0, s>>>(a, (const T*)x, (const T*)w, (const T*)bias,
+    launch_after(k_conv_bwd<T, V, K, true>, grid, 32 * kConvSub, 0, s, a, (const T*)x, (const T*)w, (const T*)bias,
                                                    (const T*)state0, (const T*)dy, dstate, (T*)dx,
                                                    dstate0, part);
   else
-    k_conv_bwd<T, V, K, false><<<grid, 32 * kConvSub, 0, s>>>(a, (const T*)x, (const T*)w, (const T*)bias,
+    launch_after(k_conv_bwd<T, V, K, false>, grid, 32 * kConvSub, 0, s, a, (const T*)x, (const T*)w, (const T*)bias,
                                                     (const T*)state0, (const T*)dy, dstate,
                                                     (T*)dx, dstate0, part);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  k_conv_reduce<<<dim3((a.C + 31) / 32, K + 1), 256, 0, s>>>(part, a.B * a.ntile, K, a.C, dw, db);
+  launch_after(k_conv_reduce, dim3((a.C + 31) / 32, K + 1), 256, 0, s, part, a.B * a.ntile, K, a.C, dw, db);
   return cudaGetLastError();
 }
 
