@@ -104,7 +104,10 @@ __device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T) {
 }
 
 // Kernels that follow one another closely are launched while the one before them ends
-// (programmatic stream serialization) and wait for it here, before they touch memory.
+// (programmatic stream serialization) and wait for it here, as their first statement,
+// until it is complete and its writes are visible: about 1 us less a launch, 27 -> 20 us
+// for the selection and attention of 64 single tokens.  No kernel lets the next one in
+// before it ends: CTAs that wait beside a running kernel cost it 1% to 15%.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>

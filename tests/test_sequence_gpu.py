@@ -348,3 +348,48 @@ def test_one_index_many_times():
         for n in ("q", "k", "v"):
             R.close(out[n], ref[n], (2 * 2.0 ** -8 * 1.02 + 2.0 ** -10) * ref[n + "_mag"], "d" + n)
         assert math.isfinite(float(lse.sum()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_calls_back_to_back(dtype):
+    """Calls that follow one another without a pause, with torch's own kernels between
+    them that write their inputs and overwrite their results' sources, give the bits that
+    the same calls give with the device idle before each one."""
+    B, T, H, G, P, N = 2, 96, 4, 2, 64, 64
+    p = _layer(B, T, H, G, P, N, dtype)
+    g = _gen(7)
+    q = torch.randn(B, T, H, P, generator=g, device="cuda").to(dtype).transpose(1, 2)
+    do = torch.randn(B, T, H, P, generator=g, device="cuda").to(dtype).transpose(1, 2)
+
+    def chain(wait):
+        out = []
+        cs = torch.zeros(B, 1, 3, H * P + 2 * G * N, dtype=dtype, device="cuda")
+        S = torch.zeros(B, H, P, N, device="cuda")
+        xbc = p["xbc"].clone()
+        for i in range(12):
+            wait()
+            y = sdm.conv_forward(xbc.unsqueeze(1), p["w"], p["b"], cs)
+            wait()
+            x, Bm, Cm = _split(y, H, G, P, N)
+            dt = p["dt"].transpose(1, 2)
+            o = sdm.ssm_forward(x, dt, p["A"], Bm, Cm, S, p["D"])
+            wait()
+            k, v = Bm, Cm
+            kc = sdm.block_pool(k, block=32)
+            wait()
+            idx = sdm.block_select(q, kc, n_sel=2, block=32)
+            wait()
+            a, lse = sdm.block_forward(q, k, v, idx, block=32, return_lse=True)
+            wait()
+            grads = sdm.block_backward(q, k, v, idx, a, lse, do, block=32)
+            wait()
+            out += [t.clone() for t in (o, S, idx, a, *grads.values())]
+            for t in (y, kc, a, lse):  # torch's kernels right behind the readers
+                t.fill_(float("nan"))
+            xbc.mul_(0.5).add_(p["xbc"], alpha=1.0 / (i + 2))
+        torch.cuda.synchronize()
+        return out
+
+    for s, t in zip(chain(torch.cuda.synchronize), chain(lambda: None)):
+        assert torch.equal(s, t)
+        assert torch.isfinite(s.float()).all()
