@@ -388,7 +388,8 @@ typedef struct sdm_ssm_views { sdm_strides x, dt, B, C, y; } sdm_ssm_views;
  * dt float32 (>= 0, after its softplus), A [H] float32 (<= 0), D [H] float32 or
  * NULL.  S_inout [B][H][d_v][d_k] float32: S_0 in, the last live state out.
  * Steps at or past lengths[b] change nothing and their y is 0.  A step with
- * dt = 0 leaves S as it is.
+ * dt = 0 leaves S as it is.  An infinity or NaN in an input leaves what does not
+ * depend on it as it is (earlier steps, other channels); what does is not finite.
  */
 SDM_API size_t sdm_ssm_workspace_bytes(const sdm_ssm_dims* dims);
 SDM_API int sdm_ssm_forward(const void* x, const float* dt, const float* A, const void* Bm,

@@ -71,6 +71,27 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&u)[PARTS
   }
 }
 
+// Whether bf16 pieces of 16 bytes in shared memory hold an infinity or NaN: 0 times them is
+// added up, in four sums that stay 0 otherwise.
+struct OddBf16 {
+  __nv_bfloat162 z[4];
+  __device__ __forceinline__ OddBf16() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = __float2bfloat162_rn(0.f);
+  }
+  __device__ __forceinline__ void add(const __nv_bfloat16* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      z[i] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), __float2bfloat162_rn(0.f), z[i]);
+  }
+  __device__ __forceinline__ bool any() const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(z);
+    return (u[0] | u[1] | u[2] | u[3]) != 0u;
+  }
+};
+
 // 16 bytes global -> shared; `in` false writes zeros and reads nothing.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
   const int n = in ? 16 : 0;

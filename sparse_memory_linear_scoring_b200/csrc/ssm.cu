@@ -195,7 +195,7 @@ k_ssm_walk(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[u][v] *= eg;
         }
-        for (int j = 0; j < t + 4; ++j) {
+        for (int j = 0; j < t; ++j) {
           float mv[4], xv[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -207,6 +207,13 @@ k_ssm_walk(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(mv[u], xv[v], acc[u][v]);
         }
+#pragma unroll
+        for (int z = 0; z < 4; ++z)  // the diagonal: a later x may be NaN, and 0 NaN is not 0
+#pragma unroll
+          for (int u = z; u < 4; ++u)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              acc[u][v] = fmaf(Ms[(t + u) * Qp + t + z], xs[(t + z) * P + p + v], acc[u][v]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           if (t0 + t + u >= a.T) break;

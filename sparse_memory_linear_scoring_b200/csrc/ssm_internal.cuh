@@ -11,6 +11,11 @@
 // for A <= 0.  g is summed in double and held, times log2 e, as a float pair:
 // near steps far into a strongly decaying chunk keep exact differences, which a
 // single float loses (g = -60 would cost 4e-6 of a weight).
+//
+// A value that is not finite stays out of what does not depend on it: a masked weight is
+// left out of a sum where 0 times that value would enter it, and the chunks' products that
+// split an operand into bf16 parts, where an infinity would become inf - inf, are taken
+// step by step for a chunk that holds such a value.
 #pragma once
 
 #include "seq_internal.cuh"
@@ -50,7 +55,8 @@ __device__ __forceinline__ void chunk_decay(const float* dts, float A, float* hi
     const double u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
-  const double ex = inc - s;
+  double ex = __shfl_up_sync(0xffffffffu, inc, 1);  // steps before the lane's: not inc - s, which
+  if (lane == 0) ex = 0.0;                          // a NaN among the lane's own would enter
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const double g = ex + v[i];

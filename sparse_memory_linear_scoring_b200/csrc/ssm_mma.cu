@@ -39,7 +39,7 @@ struct SsmTile {
   static constexpr int STAGE = X + (OUT ? 2 : 1) * BC;   // bf16 elements
   static constexpr int SB = OUT ? P * LN : 0;            // S rounded to bf16
   static constexpr int DEC = 5 * kTQ;                    // hi, lo, dt, exp(g), w
-  static constexpr size_t smem = size_t(2) * (2 * STAGE + SB) + size_t(4) * 2 * DEC;
+  static constexpr size_t smem = size_t(2) * (2 * STAGE + SB) + size_t(4) * 2 * DEC + 16;  // flags at the end
 };
 
 // Warp 0: decays of one chunk from its steps 2 lane, 2 lane + 1.
@@ -73,6 +73,7 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
   __nv_bfloat16* st = reinterpret_cast<__nv_bfloat16*>(raw);
   __nv_bfloat16* Sb = st + 2 * L::STAGE;
   float* dec = reinterpret_cast<float*>(Sb + L::SB);
+  volatile int* odd = reinterpret_cast<volatile int*>(dec + 2 * L::DEC);  // [2]: last chunk + 1 with inf or NaN in x
   constexpr int NT = 128;
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   const int seg = blockIdx.x % a.nseg, halves = a.P / P;
@@ -100,6 +101,16 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
       cp_async16(sb + 2 * (t * L::LN + e), Bm + row_off(a.sB, b, gr, tt) + e, in);
       if (OUT) cp_async16(sc + 2 * (t * L::LN + e), Cm + row_off(a.sC, b, gr, tt) + e, in);
     }
+  };
+  // whether the thread's own pieces of x, which have arrived, hold an infinity or NaN
+  auto own_odd = [&](const __nv_bfloat16* s) {
+    OddBf16 z;
+#pragma unroll
+    for (int i = 0; i < kTQ * (P / 8) / NT; ++i) {
+      const int e = tid + i * NT;
+      z.add(s + e / (P / 8) * L::LX + (e % (P / 8)) * 8);
+    }
+    return z.any();
   };
   auto dt_at = [&](int c, int i) {
     const int t = c * kTQ + 2 * lane + i;
@@ -129,7 +140,11 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
       *reinterpret_cast<uint32_t*>(p0 + 8 * L::LN) = pack_bf16(s[n][2], s[n][3]);
     }
   };
-  if (OUT) put_state();
+  if (OUT) {
+    put_state();
+    if (tid < 2) odd[tid] = 0;
+    __syncthreads();
+  }
   load(c0);
   cp_async_commit();
   if (c0 + 1 < c1) load(c0 + 1);
@@ -139,8 +154,10 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
 
   for (int c = c0; c < c1; ++c) {
     cp_async_wait<1>();
-    __syncthreads();  // chunk c's tiles, decays and bf16 state are in place
     const __nv_bfloat16* xs = st + (c & 1) * L::STAGE;
+    if (OUT && own_odd(xs)) odd[c & 1] = c + 1;
+    __syncthreads();  // chunk c's tiles, decays and bf16 state are in place
+    const bool careful = OUT && odd[c & 1] == c + 1;  // x holds inf or NaN
     __nv_bfloat16* yw = st + (c & 1) * L::STAGE + L::X + L::BC + wp * 16 * L::LN;  // C rows of the warp
     const uint32_t ax = smem_u32(xs), ab = ax + 2 * L::X, ac = ab + 2 * L::BC;
     const float* dc = dec + (c & 1) * L::DEC;
@@ -203,12 +220,35 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
               mf[2 * u] = pack_bf16(m0, m1);
               mf[2 * u + 1] = pack_bf16(m2, m3);
             }
+            if (careful && k == rt) {  // the diagonal without the masked products
+#pragma unroll 1
+              for (int z = 0; z < 16; ++z) {  // column 16 k + z of M: lane z % 8 / 2 of the row's four
+                const int from = (lane & ~3) | ((z & 7) >> 1);
+                const uint32_t wa = __shfl_sync(0xffffffffu, z < 8 ? mf[0] : mf[2], from);
+                const uint32_t wb = __shfl_sync(0xffffffffu, z < 8 ? mf[1] : mf[3], from);
+                const float ma = z & 1 ? bf16_hi(wa) : bf16_lo(wa), mb = z & 1 ? bf16_hi(wb) : bf16_lo(wb);
+                const __nv_bfloat16* xr = xs + (16 * k + z) * L::LX + 2 * q;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              uint32_t xf[4];
-              ldsm4t(xf, ax + 2 * frag_bt(lane, 16 * n, 16 * k, L::LX));
-              mma_bf16(acc[2 * n], mf, xf[0], xf[1]);
-              mma_bf16(acc[2 * n + 1], mf, xf[2], xf[3]);
+                for (int n = 0; n < 8; ++n) {
+                  const uint32_t u = *reinterpret_cast<const uint32_t*>(xr + 8 * n);
+                  if (z <= g) {
+                    acc[n][0] = fmaf(ma, bf16_lo(u), acc[n][0]);
+                    acc[n][1] = fmaf(ma, bf16_hi(u), acc[n][1]);
+                  }
+                  if (z <= g + 8) {
+                    acc[n][2] = fmaf(mb, bf16_lo(u), acc[n][2]);
+                    acc[n][3] = fmaf(mb, bf16_hi(u), acc[n][3]);
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                uint32_t xf[4];
+                ldsm4t(xf, ax + 2 * frag_bt(lane, 16 * n, 16 * k, L::LX));
+                mma_bf16(acc[2 * n], mf, xf[0], xf[1]);
+                mma_bf16(acc[2 * n + 1], mf, xf[2], xf[3]);
+              }
             }
           }
         }
@@ -285,6 +325,33 @@ k_ssm_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restri
   cp_async_wait<0>();
   float* out = OUT ? S + size_t(bh) * PN + size_t(pr) * N : slot;
   if (!OUT || a.nseg == 1) {
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bad |= !(fabsf(s[n][i]) < INFINITY);
+    if (bad) {  // inf or NaN in S, x or B, which parts do not add up to: the recurrence itself
+#pragma unroll
+      for (int n = 0; n < N / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s[n][i] = OUT ? slot[(16 * wp + g + (i >> 1) * 8) * N + 8 * n + 2 * q + (i & 1)] : 0.f;
+#pragma unroll 1
+      for (int t = c0 * kTQ; t < min(c1 * kTQ, T); ++t) {
+        const float d = dt[row_off(a.sdt, b, h, t)], at = expf(d * Ah);
+        const __nv_bfloat16* xr = x + row_off(a.sx, b, h, t) + 16 * wp + g;
+        const __nv_bfloat16* br = Bm + row_off(a.sB, b, gr, t) + 2 * q;
+        const float ua = d * __bfloat162float(xr[0]), ub = d * __bfloat162float(xr[8]);
+#pragma unroll
+        for (int n = 0; n < N / 8; ++n) {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(br + 8 * n);
+          s[n][0] = fmaf(at, s[n][0], ua * bf16_lo(u));
+          s[n][1] = fmaf(at, s[n][1], ua * bf16_hi(u));
+          s[n][2] = fmaf(at, s[n][2], ub * bf16_lo(u));
+          s[n][3] = fmaf(at, s[n][3], ub * bf16_hi(u));
+        }
+      }
+    }
 #pragma unroll
     for (int n = 0; n < N / 8; ++n) {
       float* p0 = out + (16 * wp + g) * N + 8 * n + 2 * q;

@@ -191,6 +191,22 @@ k_ssm_seg(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __restric
   if (n > 0) drain((n - 1) & 1, ((n - 1) >> 1) & 1);
   float* slot = segS + (size_t(bh) * a.nseg + seg) * P * N + 32 * quad + lane;
   const float bad = *gave_up ? NAN : 0.f;  // a wait that ran out poisons the state
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < PH; ++e) odd |= !(fabsf(F[e]) < INFINITY);
+  if (odd) {  // inf or NaN among the inputs: the recurrence itself
+#pragma unroll
+    for (int e = 0; e < PH; ++e) F[e] = 0.f;
+    const float Ah = A[h];
+#pragma unroll 1
+    for (int t = c0 * Q; t < min(c1 * Q, T); ++t) {
+      const float d = dt[row_off(a.sdt, b, h, t)], at = expf(d * Ah);
+      const float u = d * __bfloat162float(Bm[row_off(a.sB, b, gr, t) + 32 * quad + lane]);
+      const __nv_bfloat16* xr = x + row_off(a.sx, b, h, t) + half * PH;
+#pragma unroll
+      for (int e = 0; e < PH; ++e) F[e] = fmaf(at, F[e], u * __bfloat162float(xr[e]));
+    }
+  }
 #pragma unroll
   for (int e = 0; e < PH; ++e) slot[size_t(half * PH + e) * N] = F[e] + bad;
   if (tid == 0) segG[blockIdx.x] = float(later);

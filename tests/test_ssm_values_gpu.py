@@ -1,0 +1,54 @@
+"""The selective scan where its inputs hold infinities or NaN: what does not depend on such
+a value keeps its own result; what does is not finite either.  float64 walk step by step as
+the reference."""
+import pytest
+import torch
+
+import seq_ref as R
+import sparse_memory_linear_scoring_b200 as sdm
+from test_ssm_gpu import _k, _k_state, _mag, _make
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+
+# one or several chunks a segment, one or several segments, tensor cores and CUDA cores
+SHAPES = [
+    # B, H, G, T, P, N, dtype, layout
+    (1, 2, 1, 150, 64, 64, BF, "token"), (1, 2, 2, 150, 128, 128, BF, "token"),
+    (1, 2, 1, 150, 64, 128, BF, "dense"), (1, 2, 1, 150, 128, 64, BF, "token"),
+    (1, 2, 1, 150, 32, 16, BF, "token"), (1, 2, 1, 150, 64, 64, BF, "odd"),
+    (1, 2, 1, 150, 16, 32, F32, "token"), (1, 24, 2, 800, 64, 128, BF, "token"),
+    (1, 24, 2, 800, 128, 64, BF, "token"), (20, 16, 1, 150, 64, 64, BF, "token"),
+]
+
+
+def _poke(a, name, at, value):
+    """One element of one step; every head of its group reads those of Bm and Cm."""
+    t = a[name]
+    if name == "dt":
+        t[0, 0, at] = value
+    else:
+        t[0, 0, at, 11] = value
+
+
+@pytest.mark.parametrize("at,value", [(5, NAN), (70, INF), (111, NAN), (128, -INF)])
+@pytest.mark.parametrize("name", ["x", "Bm", "Cm", "dt"])
+@pytest.mark.parametrize("B,H,G,T,P,N,dtype,layout", SHAPES)
+def test_later_values_stay_out(B, H, G, T, P, N, dtype, layout, name, at, value):
+    a, _ = _make(B, H, G, T, P, N, dtype, layout)
+    if name == "dt":
+        value = NAN
+    ym, Sm, _ = R.ssm(**_mag(a))
+    _poke(a, name, at, value)
+    y, ST, _ = R.ssm(**a)
+    S = a["S"].clone()
+    got = sdm.ssm_forward(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], S, a["D"])
+    for g, r, bound, what in ((got, y, _k(dtype, T, P, N) * ym, "y"), (S, ST, _k_state(T) * Sm, "S")):
+        fin = torch.isfinite(r)
+        assert torch.equal(torch.isfinite(g), fin), "%s: finite in different places" % what
+        z = torch.zeros((), device="cuda")
+        R.close(torch.where(fin, g, z.to(g.dtype)), torch.where(fin, r, z.double()), bound, what)
+    if T <= 150:  # no decay that reaches 0: an infinity stays one in the state
+        R.close(S, ST, _k_state(T) * Sm, "S")
