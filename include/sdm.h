@@ -409,7 +409,10 @@ SDM_API int sdm_ssm_step(const void* x, const float* dt, const float* A, const v
  * of dy; grad_views.x, dt, B, C: strides of dx, ddt, dB, dC (grad_views.y is not
  * used).  dx, dB, dC have the inputs' type; ddt, dA [H], dD [H] (NULL: not
  * wanted) and dS0 [B][H][d_v][d_k] (NULL: not wanted) are float32.  dB and dC are
- * summed over their group's heads.  T >= 1.  The workspace holds the states and
+ * summed over their group's heads.  T >= 1.  An infinity or NaN in x, Bm, Cm or
+ * dy leaves what does not depend on it as it is, as in the forward pass (between a
+ * NaN of dy and a later one of x or Bm in the same 64 steps ddt may be NaN).
+ * The workspace holds the states and
  * their gradients at chunk starts and grows with T.
  */
 SDM_API size_t sdm_ssm_backward_workspace_bytes(const sdm_ssm_dims* dims);

@@ -13,7 +13,9 @@
 //     q_t = q_{t+1} + dy_t.(S_t C_t) - dt_t x_t.du_t,   q_{Q+1} = <dSin, S_Q>,
 // and both dots come from sums over W G R and from C_t.I1_t, B_j.I2_j, which are
 // at hand.  Starting the sum anew at each chunk's end keeps its rounding from
-// piling up along the sequence.  ddt_t = x_t.du_t + A q_t, dA = sum dt_t q_t,
+// piling up along the sequence.  Where S_Q is not finite (a NaN in x or B of some step),
+// the steps before that take it from the chunk's start instead, which is
+//     q_1 = exp(g_Q) <dSin, S_0> + sum_t exp(g_t) C_t.I1_t.  ddt_t = x_t.du_t + A q_t, dA = sum dt_t q_t,
 // dD = sum x_t.dy_t.
 //
 // Passes: k_ssm_local (each chunk's own contribution to the states and to their
@@ -200,10 +202,12 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const int tt = t + u, jj = j + v;
-        const float W = jj <= tt ? decay_between(hi[tt], lo[tt], hi[jj], lo[jj]) : 0.f;
-        MG[tt * Qp + jj] = W * g[u][v];
-        MR[tt * Qp + jj] = W * dts[jj] * r[u][v];
-        E[tt * Qp + jj] = W * g[u][v] * r[u][v];
+        // chosen, not multiplied by 0: a later step may hold a NaN
+        const bool in = jj <= tt;
+        const float W = in ? decay_between(hi[tt], lo[tt], hi[jj], lo[jj]) : 0.f;
+        MG[tt * Qp + jj] = in ? W * g[u][v] : 0.f;
+        MR[tt * Qp + jj] = in ? W * dts[jj] * r[u][v] : 0.f;
+        E[tt * Qp + jj] = in ? W * g[u][v] * r[u][v] : 0.f;
         if (tt == jj) dg[tt] = r[u][v];
       }
   }
@@ -249,16 +253,31 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[u][v] *= f;
     }
+    // (the diagonal by itself, for the same reason)
     if (forC) {
-      for (int j = 0; j < t + 4; ++j)
+      for (int j = 0; j < t; ++j)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float m = MR[(t + u) * Qp + j];
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(m, Bs[j * Np + e + v], acc[u][v]);
         }
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+#pragma unroll
+        for (int u = z; u < 4; ++u)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[u][v] = fmaf(MR[(t + u) * Qp + t + z], Bs[(t + z) * Np + e + v], acc[u][v]);
     } else {
-      for (int s = t; s < Q; ++s)
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+#pragma unroll
+        for (int u = 0; u <= z; ++u)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[u][v] = fmaf(MR[(t + z) * Qp + t + u], Cs[(t + z) * Np + e + v], acc[u][v]);
+      for (int s = t + 4; s < Q; ++s)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float m = MR[s * Qp + t + u];
@@ -301,7 +320,14 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[u][v] *= f;
     }
-    for (int s = t; s < Q; ++s)
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+#pragma unroll
+      for (int u = 0; u <= z; ++u)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          acc[u][v] = fmaf(MG[(t + z) * Qp + t + u], ys[(t + z) * Pp + p + v], acc[u][v]);
+    for (int s = t + 4; s < Q; ++s)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const float m = MG[s * Qp + t + u];
@@ -327,7 +353,8 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
     }
     const double yd = double(rowE[tid]) + double(ex2(hi[tid] + lo[tid])) * ci;
     const double xu = double(colE[tid]) + double(decay_between(hi[Q - 1], lo[Q - 1], hi[tid], lo[tid])) * bi;
-    double q = yd - dts[tid] * xu;
+    const double v = yd - dts[tid] * xu;
+    double q = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {  // suffix sum
       const double u = __shfl_down_sync(0xffffffffu, q, o);
@@ -336,6 +363,18 @@ k_ssm_bwd(SsmBwdArgs ba, const Tin* __restrict__ x, const float* __restrict__ dt
     double end = 0.0;
     for (int k = 0; k < kBwdThreads / 32; ++k) end += red[k];
     q += end;
+    if (!isfinite(end)) {  // a state that is not finite at the chunk's end: from its start
+      double q1 = 0.0, before = v;
+      for (size_t i = tid; i < PN; i += 32) q1 = fma(double(dSin[i]), double(S0[i]), q1);
+      q1 = exp2(double(hi[Q - 1]) + lo[Q - 1]) * warp_sum(q1) + warp_sum(double(ex2(hi[tid] + lo[tid])) * ci);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(0xffffffffu, before, o);
+        if (tid >= o) before += u;
+      }
+      before = __shfl_up_sync(0xffffffffu, before, 1);
+      if (!isfinite(q)) q = q1 - (tid == 0 ? 0.0 : before);
+    }
     if (tid < n) ddt[row_off(ba.sddt, b, h, t0 + tid)] = float(A[h] * q + xu);
     const double sA = warp_sum(double(dts[tid]) * q), sD = warp_sum(tid < n ? double(dg[tid]) : 0.0);
     if (tid == 0) {

@@ -11,6 +11,8 @@
 // widths of 64, eight of them for the splits; the tiles of x, dy, B, C and the two float32
 // states that a CTA reads (72 KB) bound it.  4 x 2048 steps, 8 heads of 64 x 64: 17 us the
 // contributions, 51 the gradients (CUDA cores: 98 and 258).
+#include <type_traits>
+
 #include "mma_dev.cuh"
 #include "ssm_internal.cuh"
 
@@ -28,6 +30,13 @@ __device__ __forceinline__ void tile_rows(uint32_t dst, int ld, const __nv_bfloa
     const bool in = t < n;
     cp_async16(dst + 2 * (t * ld + e), src + row_off(s, b, h, in ? t0 + t : 0) + e, in);
   }
+}
+
+// Adds the thread's own pieces of such a tile (they have arrived) to a check for inf and NaN.
+template <int W, int NT>
+__device__ __forceinline__ void check_rows(OddBf16& z, const __nv_bfloat16* tile, int ld) {
+#pragma unroll
+  for (int i = threadIdx.x; i < kGQ * (W / 8); i += NT) z.add(tile + i / (W / 8) * ld + (i % (W / 8)) * 8);
 }
 
 // dec: hi, lo, dt, exp(g_t), exp(g_Q - g_t), each [64]; by one warp.
@@ -109,6 +118,7 @@ k_ssm_local_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __
       }
     }
     float* out = (side == 0 ? fS : gS) + size_t(blockIdx.x) * P * N + (16 * wp + g) * N + 2 * q;
+    float all[4] = {0.f, 0.f, 0.f, 0.f};  // not finite if some result is not
 #pragma unroll
     for (int m = 0; m < N / 16; ++m) {
       float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -126,6 +136,30 @@ k_ssm_local_tile(SsmArgs a, const __nv_bfloat16* __restrict__ x, const float* __
       *reinterpret_cast<float2*>(out + 16 * m + 8 * N) = make_float2(d0[2], d0[3]);
       *reinterpret_cast<float2*>(out + 16 * m + 8) = make_float2(d1[0], d1[1]);
       *reinterpret_cast<float2*>(out + 16 * m + 8 * N + 8) = make_float2(d1[2], d1[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) all[i] += d0[i] + d1[i];
+    }
+    if (!(fabsf(all[0] + all[1]) + fabsf(all[2] + all[3]) < INFINITY)) {
+      // inf or NaN, which parts do not add up to: step by step
+      const __nv_bfloat16 *rt = t_ + side * kGQ * L::LX, *mt = t_ + 2 * kGQ * L::LX + side * kGQ * L::LN;
+      const float Ah = A[h];
+#pragma unroll 1
+      for (int m = 0; m < N / 8; ++m) {
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const int t = side == 0 ? i : n - 1 - i;
+          const float at = expf(dts[t] * Ah), f = side == 0 ? dts[t] : 1.f;
+          const float ua = f * __bfloat162float(rt[t * L::LX + 16 * wp + g]);
+          const float ub = f * __bfloat162float(rt[t * L::LX + 16 * wp + g + 8]);
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(mt + t * L::LN + 8 * m + 2 * q);
+          const float c[4] = {ua * bf16_lo(w), ua * bf16_hi(w), ub * bf16_lo(w), ub * bf16_hi(w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[e] = side == 0 ? fmaf(at, r[e], c[e]) : at * (r[e] + c[e]);
+        }
+        *reinterpret_cast<float2*>(out + 8 * m) = make_float2(r[0], r[1]);
+        *reinterpret_cast<float2*>(out + 8 * m + 8 * N) = make_float2(r[2], r[3]);
+      }
     }
   }
   if (threadIdx.x == 0) lg[blockIdx.x] = hi[kGQ - 1] + lo[kGQ - 1];
@@ -210,7 +244,11 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
   if (wp == 0) chunk_weights(dec, dt, a.sdt, b, h, t0, n, A[h]);
   split_state<P, N>(Ss, S0);
   cp_async_wait<0>();
-  __syncthreads();
+  OddBf16 z;
+  check_rows<P, NT>(z, ys, L::LX);
+  check_rows<N, NT>(z, Bs, L::LN);
+  check_rows<N, NT>(z, Cs, L::LN);
+  const bool careful = __syncthreads_or(z.any());  // inf or NaN in the operands of masked weights
 
   const int ta = 16 * rt + g, tb = ta + 8;  // the lane's rows
   {  // weights and E = W G R for rows t, columns j in [32 ch, 32 ch + 32)
@@ -254,11 +292,12 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float hj = hi[j + i], lj = lo[j + i], dj = dts[j + i];
-        const float wa = j + i <= ta ? decay_between(ha, la, hj, lj) : 0.f;
-        const float wb = j + i <= tb ? decay_between(hb, lb, hj, lj) : 0.f;
-        mg[i] = wa * gg[m][i]; mg[2 + i] = wb * gg[m][2 + i];
-        mr[i] = wa * dj * rr[m][i]; mr[2 + i] = wb * dj * rr[m][2 + i];
-        const float xa = mg[i] * rr[m][i], xb = mg[2 + i] * rr[m][2 + i];
+        // chosen, not multiplied by 0: a later step may hold a NaN
+        const bool ia = j + i <= ta, ib = j + i <= tb;
+        const float wa = decay_between(ha, la, hj, lj), wb = decay_between(hb, lb, hj, lj);
+        mg[i] = ia ? wa * gg[m][i] : 0.f; mg[2 + i] = ib ? wb * gg[m][2 + i] : 0.f;
+        mr[i] = ia ? wa * dj * rr[m][i] : 0.f; mr[2 + i] = ib ? wb * dj * rr[m][2 + i] : 0.f;
+        const float xa = ia ? mg[i] * rr[m][i] : 0.f, xb = ib ? mg[2 + i] * rr[m][2 + i] : 0.f;
         ea = fmaf(xa, dj, ea);
         eb = fmaf(xb, dj, eb);
         ce[i] = xa + xb;
@@ -357,13 +396,40 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
       }
     }
   };
+  // The diagonal tile of a product with masked weights M (m2: their second part), without
+  // the masked ones: rows t of M, or with T its columns, times the rows of `tile`.
+  auto diagonal = [&](auto& acc, auto transposed, const __nv_bfloat16* m1, const __nv_bfloat16* m2,
+                      const __nv_bfloat16* tile, int ld) {
+    constexpr bool T = decltype(transposed)::value;
+    constexpr int W = int(sizeof(acc) / sizeof(acc[0]));
+#pragma unroll 1
+    for (int z = 0; z < 16; ++z) {
+      const int r = 16 * rt + z;
+      const int oa = T ? r * L::LM + ta : ta * L::LM + r, ob = T ? r * L::LM + tb : tb * L::LM + r;
+      const float ma = __bfloat162float(m1[oa]) + (m2 ? __bfloat162float(m2[oa]) : 0.f);
+      const float mb = __bfloat162float(m1[ob]) + (m2 ? __bfloat162float(m2[ob]) : 0.f);
+      const bool ia = T ? z >= g : z <= g, ib = T ? z >= g + 8 : z <= g + 8;
+#pragma unroll
+      for (int m = 0; m < W; ++m) {
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(tile + r * ld + 8 * m + 2 * q);
+        if (ia) {
+          acc[m][0] = fmaf(ma, bf16_lo(u), acc[m][0]);
+          acc[m][1] = fmaf(ma, bf16_hi(u), acc[m][1]);
+        }
+        if (ib) {
+          acc[m][2] = fmaf(mb, bf16_lo(u), acc[m][2]);
+          acc[m][3] = fmaf(mb, bf16_hi(u), acc[m][3]);
+        }
+      }
+    }
+  };
   {  // dC_t = exp(g_t) I1_t + sum_j MR_tj B_j
     float acc[NH / 8][4];
     times_state(acc, ay);
     dot_scale(acc, Cs, dotC, eg[ta], eg[tb]);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k <= rt) {
+      if (k < rt || (k == rt && !careful)) {
         uint32_t af[4], cf[4];
         ldsm4(af, ar + 2 * frag_a(lane, 16 * rt, 16 * k, L::LM));
         ldsm4(cf, a2 + 2 * frag_a(lane, 16 * rt, 16 * k, L::LM));
@@ -377,6 +443,7 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
           mma_bf16(acc[2 * m + 1], af, bf[2], bf[3]);
         }
       }
+    if (careful) diagonal(acc, std::false_type(), MR, M2, Bs + n0, L::LN);
     put(acc, dC, ba.sdC, w.pC);
   }
   __syncthreads();  // everyone is done with S_0
@@ -399,7 +466,7 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
     dot_scale(acc, Bs, dotB, dts[ta] * ej[ta], dts[tb] * ej[tb]);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k >= rt) {
+      if (k > rt || (k == rt && !careful)) {
         uint32_t af[4], cf[4];
         ldsm4t(af, ar + 2 * frag_at(lane, 16 * rt, 16 * k, L::LM));
         ldsm4t(cf, a2 + 2 * frag_at(lane, 16 * rt, 16 * k, L::LM));
@@ -413,6 +480,7 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
           mma_bf16(acc[2 * m + 1], af, bf[2], bf[3]);
         }
       }
+    if (careful) diagonal(acc, std::true_type(), MR, M2, Cs + n0, L::LN);
     put(acc, dB, ba.sdB, w.pB);
   }
   {  // dx_j = dt_j (e_j dSin B_j + sum_t MG_tj dy_t) + D dy_j
@@ -440,7 +508,7 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k >= rt) {
+      if (k > rt || (k == rt && !careful)) {
         uint32_t af[4];
         ldsm4t(af, ag + 2 * frag_at(lane, 16 * rt, 16 * k, L::LM));
 #pragma unroll
@@ -451,6 +519,7 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
           mma_bf16(acc[2 * m + 1], af, bf[2], bf[3]);
         }
       }
+    if (careful) diagonal(acc, std::true_type(), MG, static_cast<const __nv_bfloat16*>(nullptr), ys + p0, L::LX);
     const float Dh = D ? D[h] : 0.f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -491,7 +560,25 @@ k_ssm_grad(SsmBwdArgs ba, const __nv_bfloat16* __restrict__ x, const float* __re
     double end = 0.0;
 #pragma unroll
     for (int k = 0; k < kGradWarps; ++k) end += red[k];
-    const double q1 = (suf - s) + v[1] + end, q0 = suf + end;
+    const double after = __shfl_down_sync(0xffffffffu, suf, 1);
+    double q1 = (lane == 31 ? 0.0 : after) + v[1] + end, q0 = suf + end;
+    if (!isfinite(end)) {  // a state that is not finite at the chunk's end: from its start
+      double qs = 0.0, before = s;
+      for (int i = lane; i < int(PN); i += 32) qs = fma(double(dSin[i]), double(S0[i]), qs);
+      double cd = 0.0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) cd += double(eg[2 * lane + i]) * (dotC[2 * lane + i] + dotC[kGQ + 2 * lane + i]);
+      qs = exp2(double(hi[kGQ - 1]) + lo[kGQ - 1]) * warp_sum(qs) + warp_sum(cd);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += u;
+      }
+      before = __shfl_up_sync(0xffffffffu, before, 1);
+      if (lane == 0) before = 0.0;
+      if (!isfinite(q0)) q0 = qs - before;
+      if (!isfinite(q1)) q1 = qs - before - v[0];
+    }
     const float Ah = A[h];
     double sA = 0.0, sD = 0.0;
 #pragma unroll

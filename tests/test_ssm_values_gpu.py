@@ -52,3 +52,32 @@ def test_later_values_stay_out(B, H, G, T, P, N, dtype, layout, name, at, value)
         R.close(torch.where(fin, g, z.to(g.dtype)), torch.where(fin, r, z.double()), bound, what)
     if T <= 150:  # no decay that reaches 0: an infinity stays one in the state
         R.close(S, ST, _k_state(T) * Sm, "S")
+
+
+def _grads(a, dy, dS):
+    return sdm.ssm_backward(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], a["S"], dy, dS, D=a["D"])
+
+
+@pytest.mark.parametrize("at,value", [(5, NAN), (70, INF), (111, NAN), (128, -INF)])
+@pytest.mark.parametrize("name", ["x", "Bm", "Cm", "dy"])
+@pytest.mark.parametrize("B,H,G,T,P,N,dtype,layout", SHAPES[:7])
+def test_gradients_stay_apart(B, H, G, T, P, N, dtype, layout, name, at, value):
+    a, g = _make(B, H, G, T, P, N, dtype, layout)
+    dy = torch.randn(B, T, H, P, generator=g, device="cuda").to(dtype).transpose(1, 2)
+    dS = torch.randn(B, H, P, N, generator=g, device="cuda") * 0.3
+    args = [a[n] for n in ("x", "dt", "A", "Bm", "Cm", "S")]
+    mag = R.ssm_grads(*args, dy, dS, a["D"], magnitude=True)
+    _poke({**a, "dy": dy}, name, at, value)
+    ref = R.ssm_grads(*args, dy, dS, a["D"])
+    out = _grads(a, dy, dS)
+    k16 = _k(dtype, T, P, N) + P * R.ADD
+    k32 = (64 + 2 * max(P, N) + T / 32 + 16) * R.ADD + 2.0 ** -17
+    # dt's gradient is a running sum over a chunk of at most 64 steps that may be taken from
+    # either end: the terms of both count
+    mag["dt"] = 2 * torch.nn.functional.max_pool1d(mag["dt"].float().flatten(0, 1)[None], 129, 1, 64)[0].view_as(mag["dt"]).double()
+    for n in ("x", "Bm", "Cm", "dt", "S0"):
+        fin = torch.isfinite(ref[n])
+        assert torch.equal(torch.isfinite(out[n]), fin), "d%s: finite in different places" % n
+        z = torch.zeros((), device="cuda")
+        R.close(torch.where(fin, out[n], z.to(out[n].dtype)), torch.where(fin, ref[n], z.double()),
+                (k16 if n in ("x", "Bm", "Cm") else k32) * mag[n], "d" + n)
