@@ -472,7 +472,8 @@ SDM_API int sdm_block_forward(const void* q, const void* k, const void* v, const
 /*
  * Gradients of sdm_block_forward at its lists, in the inputs' type; o and lse as it
  * wrote them.  grad_views.q, k, v: strides of dq, dk, dv; grad_views.o: of d_o.
- * All Tk rows of dk and dv are written.  Tq >= 1.
+ * All Tk rows of dk and dv are written.  Tq >= 1.  A query or an incoming gradient
+ * that is not finite reaches dk and dv of the keys that the query sees, no others.
  */
 SDM_API size_t sdm_block_backward_workspace_bytes(const sdm_block_dims* dims);
 SDM_API int sdm_block_backward(const void* q, const void* k, const void* v, const int32_t* idx,

@@ -69,6 +69,7 @@ k_blk_kv(BlkArgs a, BlkPlan pl, const Tin* __restrict__ q, const Tin* __restrict
       }
     }
     *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+    return !(fabsf(f[0]) + fabsf(f[1]) + fabsf(f[2]) + fabsf(f[3]) < INFINITY);
   };
   for (int i = tid; i < 32 * (D / 4); i += kKvThreads) {
     const int kk = i / (D / 4), c = (i % (D / 4)) * 4;
@@ -103,15 +104,17 @@ k_blk_kv(BlkArgs a, BlkPlan pl, const Tin* __restrict__ q, const Tin* __restrict
       rd[tid] = in ? delta[at] : 0.f;
     }
     __syncthreads();
+    bool odd = false;
 #pragma unroll 4
     for (int i = tid; i < kKvRows * (D / 4); i += kKvThreads) {
       const int r = i / (D / 4), cc = (i % (D / 4)) * 4;
       const bool in = rt[r] >= 0;
       const int t = in ? rt[r] : 0;
-      four(q + row_off(a.sq, b, rh[r], t) + cc, in, qs + r * D + cc);
-      four(d_o + row_off(sdo, b, rh[r], t) + cc, in, gs + r * D + cc);
+      odd |= four(q + row_off(a.sq, b, rh[r], t) + cc, in, qs + r * D + cc);
+      odd |= four(d_o + row_off(sdo, b, rh[r], t) + cc, in, gs + r * D + cc);
     }
-    __syncthreads();
+    // rows with inf or NaN: 0 times them is not 0, so they leave out the keys they do not see
+    const bool careful = __syncthreads_or(odd);
     {  // warp wp takes rows 4 wp .. 4 wp + 3, lane takes a key
       float s[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -145,6 +148,7 @@ k_blk_kv(BlkArgs a, BlkPlan pl, const Tin* __restrict__ q, const Tin* __restrict
       const float4 y = *reinterpret_cast<const float4*>(gs + r * D + c);
 #pragma unroll
       for (int u = 0; u < NA; ++u) {
+        if (careful && k0 + ks + u > pos0 + rt[r]) continue;
         const float w = ds[r * 36 + ks + u], z = ps[r * 36 + ks + u];
         ak[u][0] = fmaf(w, x.x, ak[u][0]); ak[u][1] = fmaf(w, x.y, ak[u][1]);
         ak[u][2] = fmaf(w, x.z, ak[u][2]); ak[u][3] = fmaf(w, x.w, ak[u][3]);

@@ -41,7 +41,7 @@ struct GradTile {
   static constexpr int ST = D <= 64 ? 2 : 1;   // row tiles in flight; at 128 a second CTA an SM does more
   static constexpr int LD = D + 8, LP = KT + 8;
   static constexpr int KV = KT * LD, RW = kGradTile * LD, PS = kGradTile * LP;
-  static constexpr size_t smem = size_t(2) * (2 * KV + ST * 2 * RW + 3 * PS) + 16;
+  static constexpr size_t smem = size_t(2) * (2 * KV + ST * 2 * RW + 3 * PS) + 32;
 };
 
 template <int D, int KT>
@@ -59,6 +59,7 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
   __nv_bfloat16* Ds = Ps + L::PS;
   __nv_bfloat16* Es = Ds + L::PS;                  // second part of dS
   uint32_t* odd = reinterpret_cast<uint32_t*>(Es + L::PS);  // keys with inf or NaN in K
+  uint32_t* rowodd = odd + 4;  // [4]: by warp, its rows with inf or NaN in Q or dO and masked keys
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   const int g = lane >> 2, qd = lane & 3;
   const int per = a.bs / KT, sub = blockIdx.x % per;
@@ -201,6 +202,30 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
         *reinterpret_cast<uint32_t*>(Es + at + 8 * L::LP) = s1[1];
       }
     }
+    // A masked weight is 0, but 0 times an infinite or NaN query or gradient is not: such
+    // elements are taken out of the rows and added, by hand, to the keys that their row sees.
+    uint32_t mine = 0;
+    if (masked) {
+      __nv_bfloat16* rows_ = Rs + st * 2 * L::RW + wp * 16 * L::LD;
+#pragma unroll
+      for (int i = lane; i < 16 * (D / 8); i += 32) {
+        const int rr = i / (D / 8), c = (i % (D / 8)) * 8;
+        OddBf16 z;
+        z.add(rows_ + rr * L::LD + c);
+        z.add(rows_ + L::RW + rr * L::LD + c);
+        if (z.any()) mine |= 1u << rr;
+      }
+      mine = __reduce_or_sync(0xffffffffu, mine) & __ballot_sync(0xffffffffu, me.keys < KT) & 0xffffu;
+      if (mine) {
+        for (int i = lane; i < 16 * D; i += 32) {
+          const int rr = i / D, at = rr * L::LD + i % D;
+          if (!(mine >> rr & 1)) continue;
+          if (!(fabsf(__bfloat162float(rows_[at])) < INFINITY)) rows_[at] = __float2bfloat16_rn(0.f);
+          if (!(fabsf(__bfloat162float(rows_[L::RW + at])) < INFINITY)) rows_[L::RW + at] = __float2bfloat16_rn(0.f);
+        }
+      }
+    }
+    if (lane == 0) rowodd[wp] = mine;
     __syncthreads();  // all rows' Q, dO, P and dS are in place
 #pragma unroll
     for (int kk = 0; kk < kGradTile; kk += 16) {
@@ -219,6 +244,29 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
         mma_bf16(gk[2 * n + 1], tf, bf[2], bf[3]);
         mma_bf16(gk[2 * n], sf, bf[0], bf[1]);
         mma_bf16(gk[2 * n + 1], sf, bf[2], bf[3]);
+      }
+    }
+    if (rowodd[0] | rowodd[1] | rowodd[2] | rowodd[3]) {
+#pragma unroll 1
+      for (int rr = 0; rr < kGradTile; ++rr) {
+        if (!(rowodd[rr >> 4] >> (rr & 15) & 1)) continue;
+        const int row = base + rr, en = a.by_R.div(row), h = grp * a.R + row - en * a.R;
+        const int t = a.q0 + a.by_sel.div(entry[en]), n = pos0 + t - k0 + 1;  // keys it sees
+        const __nv_bfloat16 *qr = q + row_off(a.sq, b, h, t) + cp, *dr = d_o + row_off(sdo, b, h, t) + cp;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = 16 * ks + g + 8 * u, at = rr * L::LP + key;
+          if (key >= n) continue;
+          const float pk = __bfloat162float(Ps[at]), sk = __bfloat162float(Ds[at]) + __bfloat162float(Es[at]);
+#pragma unroll
+          for (int m = 0; m < DP / 8; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x = __bfloat162float(qr[8 * m + 2 * qd + i]), y = __bfloat162float(dr[8 * m + 2 * qd + i]);
+              if (!(fabsf(x) < INFINITY)) gk[m][2 * u + i] = fmaf(sk, x, gk[m][2 * u + i]);
+              if (!(fabsf(y) < INFINITY)) gv[m][2 * u + i] = fmaf(pk, y, gv[m][2 * u + i]);
+            }
+        }
       }
     }
     float acc[D / 8][4];

@@ -1,0 +1,45 @@
+"""Block-selected attention where its values are unusual: infinities and NaN in queries and
+incoming gradients, channels of very different sizes, keys that share a large component."""
+import pytest
+import torch
+
+import seq_ref as R
+import sparse_memory_linear_scoring_b200 as sdm
+from test_block_gpu import _make
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("name", ["q", "do"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,block,Tq,Tk", [(64, 64, 200, 200), (64, 32, 20, 200), (128, 128, 200, 200),
+                                          (32, 64, 300, 333), (64, 128, 900, 900), (128, 32, 150, 150)])
+def test_queries_stay_out_of_later_keys(d, block, Tq, Tk, dtype, name, value):
+    """A query or an incoming gradient that is not finite reaches dK and dV of the keys that
+    the query sees and leaves the others', those behind it in its own block among them."""
+    q, k, v, g = _make(1, 4, 2, Tq, Tk, d, dtype)
+    idx = R.select(q, R.pool(k, block), 3, block, Tk)
+    do = torch.randn(q.shape, generator=g, device="cuda").to(dtype)
+    o, lse = sdm.block_forward(q, k, v, idx, block=block, return_lse=True)
+    good = sdm.block_backward(q, k, v, idx, o, lse, do, block=block)
+    seen = torch.zeros(2, Tk, dtype=torch.bool, device="cuda")
+    c = R.counts(idx, block, Tk, R.positions(1, Tq, Tk, None, q.device))[0] > 0
+    for h, t in ((1, Tq // 2), (2, Tq - 18), (0, 3)):
+        (q if name == "q" else do)[0, h, t, 5] = value
+        seen[h // 2] |= c[h // 2, t]
+    assert not seen[0, Tk - Tq + Tq // 2 + 1:].all() and seen.any(1).all()
+    o, lse = sdm.block_forward(q, k, v, idx, block=block, return_lse=True)
+    got = sdm.block_backward(q, k, v, idx, o, lse, do, block=block)
+    for n in ("k", "v"):
+        for gr in range(2):
+            a, b, s = got[n][0, gr], good[n][0, gr], seen[gr]
+            assert torch.equal(a[~s], b[~s]), "d%s of group %d" % (n, gr)
+            if name == "do" and n == "v":  # one column of dO
+                assert torch.equal(a[:, :5], b[:, :5]) and torch.equal(a[:, 6:], b[:, 6:])
+                assert not torch.isfinite(a[s, 5]).any()
+            elif value != value or name == "do":
+                assert not torch.isfinite(a[s]).any()
