@@ -11,7 +11,8 @@
 // norm; the result's own rounding is 0.0017).  Each warp owns 16 rows for P, dS and dQ, and
 // 16 keys (or 16 keys and half the columns) for dK and dV, whose operands it takes
 // transposed from shared memory.  A row's dQ is a sum over its list: parts are halves
-// scaled by their largest element (2^-12 beside the result's 2^-9), joined in list order.
+// scaled by their largest element to 2^15 (2^-12 beside the result's 2^-9, down to 2^-29 of
+// that element), joined in list order.
 // dK and dV of one item are float32 parts, joined in item order: no atomics, equal calls
 // give equal bits.
 // delta = do.o comes from o as the forward wrote it, in bf16, and what that is off, e, is
@@ -341,9 +342,9 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
       xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, o));
       xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, o));
     }
-    xa = fmaxf(xa, 2.3509887e-38f);  // 2^-125: its reciprocal is still finite
-    xb = fmaxf(xb, 2.3509887e-38f);
-    const float va = 1.f / xa, vb = 1.f / xb;
+    xa = fmaxf(xa, 7.7037198e-34f);  // 2^-110: the factor stays finite
+    xb = fmaxf(xb, 7.7037198e-34f);
+    const float va = 32768.f / xa, vb = 32768.f / xb;
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       ea += __shfl_xor_sync(0xffffffffu, ea, o);
@@ -385,13 +386,13 @@ k_blk_grad(BlkArgs a, BlkBwdWs w, const __nv_bfloat16* __restrict__ q,
       ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
       kb = fmaxf(kb, __shfl_xor_sync(0xffffffffu, kb, o));
     }
-    ka = fminf(fmaxf(ka, 2.3509887e-38f), 1.7e38f);
-    kb = fminf(fmaxf(kb, 2.3509887e-38f), 1.7e38f);
-    const float fa = 1.f / ka, fb = 1.f / kb;
+    ka = fminf(fmaxf(ka, 7.7037198e-34f), 1.7e38f);
+    kb = fminf(fmaxf(kb, 7.7037198e-34f), 1.7e38f);
+    const float fa = 256.f / ka, fb = 256.f / kb;  // 8-bit floats reach 448
     const size_t oa = __shfl_sync(0xffffffffu, me.place, g), ob = __shfl_sync(0xffffffffu, me.place, g + 8);
     if (qd == 0) {
-      if (ra < r1) w.mul[oa] = make_float4(xa, ka, ea, 0.f);
-      if (rb < r1) w.mul[ob] = make_float4(xb, kb, eb, 0.f);
+      if (ra < r1) w.mul[oa] = make_float4(xa * (1.f / 32768.f), ka * (1.f / 256.f), ea, 0.f);
+      if (rb < r1) w.mul[ob] = make_float4(xb * (1.f / 32768.f), kb * (1.f / 256.f), eb, 0.f);
     }
     __syncwarp();  // the warp has sent its parts of dQ
     unsigned short* bytes = reinterpret_cast<unsigned short*>(stage);  // rows of LD halves again

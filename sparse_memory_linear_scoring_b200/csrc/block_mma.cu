@@ -9,9 +9,9 @@
 // running maximum.  What this costs is a partial result per (query, slot, head) --
 // d halves, a log-sum-exp and a scale, written here and read once by the join:
 //     o = sum_s exp(lse_s - lse) o_s,   lse = log sum_s exp(lse_s).
-// Partials are halves scaled by the row's largest element: 11 significant bits, an
-// error of 2^-12 beside the 2^-9 of the weights' and the result's bf16; float32
-// partials would double the bytes that bound this path.
+// Partials are halves scaled by the row's largest element to 2^15: 11 significant bits
+// for elements down to 2^-29 of it, an error of 2^-12 beside the 2^-9 of the weights' and
+// the result's bf16; float32 partials would double the bytes that bound this path.
 #include <cuda_fp16.h>
 
 #include "block_internal.cuh"

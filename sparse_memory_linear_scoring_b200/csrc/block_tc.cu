@@ -271,8 +271,9 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
       for (int c = 0; c < D; ++c)
         if (fabsf(acc[c]) < INFINITY) xm = fmaxf(xm, fabsf(acc[c]));
     }
-    xm = fmaxf(xm, 2.3509887e-38f);  // 2^-125: its reciprocal is still finite
-    const float f = 1.f / xm;
+    xm = fmaxf(xm, 7.7037198e-34f);  // 2^-110: the factor stays finite
+    // the largest becomes 2^15: halves keep all their bits down to 2^-29 of it
+    const float f = 32768.f / xm;
     unsigned char* orow = work + tid * L::OP;
 #pragma unroll
     for (int c = 0; c < D; c += 8) {
@@ -286,7 +287,7 @@ k_blk_tc(BlkArgs a, BlkFwdWs w, const __nv_bfloat16* __restrict__ q, const __nv_
     }
     if (base + tid < r1) {
       // a wait that ran out poisons the row
-      float2 ml = l == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(m + log2f(l), xm / l);
+      float2 ml = l == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(m + log2f(l), xm * (1.f / 32768.f) / l);
       if (*gave_up) ml = make_float2(NAN, NAN);
       w.ml[place] = ml;
     }

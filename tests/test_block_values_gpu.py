@@ -5,7 +5,7 @@ import torch
 
 import seq_ref as R
 import sparse_memory_linear_scoring_b200 as sdm
-from test_block_gpu import _make
+from test_block_gpu import _k, _make
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,26 @@ def test_queries_stay_out_of_later_keys(d, block, Tq, Tk, dtype, name, value):
                 assert not torch.isfinite(a[s, 5]).any()
             elif value != value or name == "do":
                 assert not torch.isfinite(a[s]).any()
+
+
+@pytest.mark.parametrize("Tq", [1, 20, 1500])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,block", [(64, 64), (128, 32), (32, 128)])
+def test_channels_of_different_sizes(d, block, dtype, Tq):
+    """Values, and keys for dQ, whose channels differ by up to 2^23: each channel of the
+    result is as exact as its own terms allow."""
+    q, k, v, g = _make(2, 12, 2, Tq, 1777, d, dtype, "token")
+    size = 2.0 ** -(torch.arange(d, device="cuda") % 24).float()
+    v.copy_((v.float() * size).to(dtype))
+    k.copy_((k.float() * size).to(dtype))
+    idx = R.select(q, R.pool(k, block), 24, block, 1777)
+    do = torch.randn(q.shape, generator=g, device="cuda").to(dtype)
+    ref = R.block_attention(q, k, v, idx, block, 1.0, None, do)
+    o, lse = sdm.block_forward(q, k, v, idx, block=block, scale=1.0, return_lse=True)
+    R.close(o, ref["o"], _k(dtype, d, ref) * ref["o_mag"], "o")
+    out = sdm.block_backward(q, k, v, idx, o, lse, do, block=block, scale=1.0)
+    # as the other gradients: scores twice, one rounding of P or dS, one of o in do.o
+    k1 = 4 * d * R.ADD * float(ref["smag"].max()) + 2.0 ** -18 + (300 + 24 * 8) * R.ADD
+    if dtype == BF:
+        k1 += 2 * 2.0 ** -8 * 1.02
+    R.close(out["q"], ref["q"], k1 * ref["q_mag"], "dq")
