@@ -6,6 +6,9 @@
 //   lse = log sum exp(s_k);  no key: o = 0, lse = -inf.
 //   backward: P_k = exp(s_k - lse), dP_k = do.v_k, ds_k = P_k (dP_k - do.o) scale,
 //   dq = sum ds_k k_k.
+// With o rounded to bf16, do.o is off by some e, and dq by e sum P_k k_k: so sum P_k k_k and
+// e = sum_k P_k (dP_k - do.o), which would be 0, are summed too and their product taken off,
+// and the delta that is left for dk and dv gets e.
 //
 // A query reads n_sel blocks of keys and values once for up to 4 heads that share
 // them, which is 2 flops a byte and head: loads bound it.  So there are no shared
@@ -80,8 +83,9 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
   wait_for_previous();
   constexpr int V = 16 / int(sizeof(Tin)), LN = D / V, KP = 32 / LN;
   constexpr int NB = LN < 8 ? LN : 8, NG = LN / NB;  // rows loaded together, such groups
-  __shared__ float part[kRowWarps][RH][D];
-  __shared__ float pm[kRowWarps][RH], pl[kRowWarps][RH];
+  constexpr bool FIX = BWD && sizeof(Tin) == 2;  // o is rounded: e comes off again
+  __shared__ float part[kRowWarps][RH][D], pk[FIX ? kRowWarps : 1][RH][FIX ? D : 1];
+  __shared__ float pm[kRowWarps][RH], pl[kRowWarps][RH], pd[RH];  // backward: pl for e, pd for do.o
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int rank = blockIdx.x % cs;
   long long i = blockIdx.x / cs;
@@ -113,16 +117,20 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
       const size_t at = ((size_t)b * a.H + h0 + (in ? r : 0)) * a.Tq + t;
       const float x = in ? lse[at] : -INFINITY;
       ls[r] = x == -INFINITY ? INFINITY : x * kLog2e;  // weights of a row without keys are 0
-      if (rank == 0 && threadIdx.x == 0 && in) delta[at] = s;
+      if (FIX) {
+        if (threadIdx.x == 0) pd[r] = s;
+      } else if (rank == 0 && threadIdx.x == 0 && in) {
+        delta[at] = s;
+      }
     }
   }
-  float acc[RH][V], m[RH], l[RH];
+  float acc[RH][V], m[RH], l[RH], ak[FIX ? RH : 1][V];
 #pragma unroll
   for (int r = 0; r < RH; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[r][e] = 0.f;
+    for (int e = 0; e < V; ++e) acc[r][e] = ak[FIX ? r : 0][e] = 0.f;
   }
   const int32_t* list = idx + ((size_t)bg * a.Tq + t) * a.n_sel;
   const int per = a.bs / 32, pieces = a.n_sel * per;
@@ -133,7 +141,7 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
     const long long key0 = (long long)j * a.bs + k0;
     const Tin* kp = k + row_off(a.sk, b, g, 0) + key0 * a.sk.t + c;
     const Tin* vp = v + row_off(a.sv, b, g, 0) + key0 * a.sv.t + c;
-    float s[RH], dp[BWD ? RH : 1];
+    float s[RH], dp[BWD ? RH : 1], w[FIX ? RH : 1];
     // scores (and do.v): each group of NB row loads leaves one value a lane
     auto dots = [&](const Tin* base, long long st, const float (&x)[RH][V], int on, float (&out)[RH]) {
       float gsum[RH][NG];
@@ -189,8 +197,14 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
     if constexpr (BWD) {
       dots(vp, a.sv.t, gf, vec & 8, dp);
 #pragma unroll
-      for (int r = 0; r < RH; ++r)
-        s[r] = mine ? exp2f(s[r] - ls[r]) * (dp[r] - dl[r]) * a.scale : 0.f;
+      for (int r = 0; r < RH; ++r) {
+        const float P = mine ? exp2f(s[r] - ls[r]) : 0.f, x = mine ? P * (dp[r] - dl[r]) : 0.f;
+        s[r] = x * a.scale;
+        if constexpr (FIX) {
+          w[r] = P;
+          l[r] += x;
+        }
+      }
     } else {
 #pragma unroll
       for (int r = 0; r < RH; ++r) {
@@ -224,9 +238,15 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
         piece_f32<Tin>(raw[z], f);
 #pragma unroll
         for (int r = 0; r < RH; ++r) {
-          const float w = __shfl_sync(0xffffffffu, s[r], (lane & ~(LN - 1)) | (u * NB + z));
+          const int from = (lane & ~(LN - 1)) | (u * NB + z);
+          const float y = __shfl_sync(0xffffffffu, s[r], from);
 #pragma unroll
-          for (int e = 0; e < V; ++e) acc[r][e] = fmaf(w, f[e], acc[r][e]);
+          for (int e = 0; e < V; ++e) acc[r][e] = fmaf(y, f[e], acc[r][e]);
+          if constexpr (FIX) {
+            const float P = __shfl_sync(0xffffffffu, w[r], from);
+#pragma unroll
+            for (int e = 0; e < V; ++e) ak[r][e] = fmaf(P, f[e], ak[r][e]);
+          }
         }
       }
     }
@@ -237,11 +257,17 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
 #pragma unroll
     for (int w = LN; w < 32; w <<= 1)
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[r][e] += __shfl_xor_sync(0xffffffffu, acc[r][e], w);
+      for (int e = 0; e < V; ++e) {
+        acc[r][e] += __shfl_xor_sync(0xffffffffu, acc[r][e], w);
+        if constexpr (FIX) ak[r][e] += __shfl_xor_sync(0xffffffffu, ak[r][e], w);
+      }
     if (sub == 0)
 #pragma unroll
-      for (int e = 0; e < V; ++e) part[wp][r][c + e] = acc[r][e];
-    if constexpr (!BWD) {
+      for (int e = 0; e < V; ++e) {
+        part[wp][r][c + e] = acc[r][e];
+        if constexpr (FIX) pk[wp][r][c + e] = ak[r][e];
+      }
+    if constexpr (!BWD || FIX) {
       l[r] = warp_sum(l[r]);
       if (lane == 0) {
         pm[wp][r] = m[r];
@@ -253,7 +279,7 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
   if (cs > 1) cl.sync(); else __syncthreads();
   for (int e = rank * kRowWarps * 32 + threadIdx.x; e < nh * D; e += cs * kRowWarps * 32) {
     const int r = e / D, col = e % D;
-    float mx = -INFINITY, x = 0.f, sum = 0.f;
+    float mx = -INFINITY, x = 0.f, sum = 0.f, sk = 0.f;
     if constexpr (!BWD) {
       for (int w = 0; w < cs; ++w) {
         const float* om = cs > 1 ? cl.map_shared_rank(&pm[0][0], w) : &pm[0][0];
@@ -269,7 +295,12 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
 #pragma unroll
       for (int y = 0; y < kRowWarps; ++y) {
         const float z = op[(y * RH + r) * D + col];
-        if constexpr (BWD) {
+        if constexpr (FIX) {
+          const float* ok = cs > 1 ? cl.map_shared_rank(&pk[0][0][0], w) : &pk[0][0][0];
+          x += z;
+          sk += ok[(y * RH + r) * D + col];
+          sum += ol[y * RH + r];
+        } else if constexpr (BWD) {
           x += z;
         } else {
           const float f = exp2f(om[y * RH + r] - mx);
@@ -279,6 +310,10 @@ k_blk_row(BlkArgs a, const Tin* __restrict__ q, const Tin* __restrict__ k, const
       }
     }
     if constexpr (BWD) {
+      if constexpr (FIX) {
+        x -= sum * a.scale * sk;
+        if (col == 0) delta[((size_t)b * a.H + h0 + r) * a.Tq + t] = pd[r] + sum;
+      }
       dq[row_off(sdq, b, h0 + r, t) + col] = from_f32<Tin>(x);
     } else {
       o[row_off(a.so, b, h0 + r, t) + col] = from_f32<Tin>(sum == 0.f ? 0.f : x / sum);

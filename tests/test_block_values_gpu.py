@@ -66,3 +66,26 @@ def test_channels_of_different_sizes(d, block, dtype, Tq):
     if dtype == BF:
         k1 += 2 * 2.0 ** -8 * 1.02
     R.close(out["q"], ref["q"], k1 * ref["q_mag"], "dq")
+
+
+def _norm(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+@pytest.mark.parametrize("H,G,Tq,Tk,d,block,layout", [
+    (8, 2, 1, 600, 64, 64, "dense"), (8, 8, 20, 600, 64, 64, "token"), (4, 2, 300, 600, 128, 32, "odd"),
+    (8, 2, 600, 600, 64, 64, "token"), (12, 2, 900, 900, 128, 64, "token"), (6, 3, 500, 500, 32, 128, "dense")])
+def test_keys_with_a_common_part(H, G, Tq, Tk, d, block, layout):
+    """A row of dS sums to zero, so what a query's keys share drops out of dQ.  Keys 8 units
+    off centre: the result's rounding makes 0.0017 of the norm; what is left of dS behind its
+    two parts, 2^-17, of do.o behind its correction, 2^-4 of 0.0022, and of the parts, 2^-12,
+    enters eight times as large: below 0.004.  One part of dS or no correction: about 0.02."""
+    q, k, v, g = _make(2, H, G, Tq, Tk, d, BF, layout)
+    k += 8 * torch.sign(torch.randn(d, generator=g, device="cuda")).to(BF)
+    q *= 0.25
+    idx = R.select(q, R.pool(k, block), 6, block, Tk)
+    do = torch.randn(q.shape, generator=g, device="cuda").to(BF)
+    ref = R.block_attention(q, k, v, idx, block, d ** -0.5, None, do)
+    o, lse = sdm.block_forward(q, k, v, idx, block=block, return_lse=True)
+    out = sdm.block_backward(q, k, v, idx, o, lse, do, block=block)
+    assert _norm(out["q"], ref["q"]) <= 0.004
