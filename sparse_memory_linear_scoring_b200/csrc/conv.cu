@@ -24,13 +24,22 @@ struct ConvArgs {
   sdm_strides sx, sy;
 };
 
-// 1 / (1 + exp(-p)) on the special function unit, 2^-22 relative; 0 below p = -87.3,
-// where it is less than 2^-126.
-__device__ __forceinline__ float sigmoid(float p) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p * -kLog2e));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return r;
+// s = 1 / (1 + exp(-p)) and c = 1 - s on the special function unit; s is 0 below
+// p = -87.3, where it is less than 2^-126.  The rounding of p log2 e moves exp by |p| 2^-24
+// of itself, which beside bf16 results (2^-9) does not count.  For float32 its remainder is
+// carried into exp (2^-21 of s wherever p lies), and c is exp(-p) s where 1 - s would
+// keep only s's last bits.
+template <typename T>
+__device__ __forceinline__ void sigmoid(float p, float& s, float& c) {
+  const float x = p * -kLog2e;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  if (sizeof(T) == 4 && fabsf(p) < 128.f) {
+    const float rest = fmaf(p, -kLog2e, -x) + p * -1.9259629911e-8f;  // log2 e is kLog2e + 1.93e-8
+    e = fmaf(e, rest * 0.69314718056f, e);
+  }
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  c = sizeof(T) == 4 && p > 0.f ? e * s : 1.f - s;
 }
 
 // acc += a * b over V channels, two to an instruction.
@@ -138,7 +147,11 @@ k_conv_fwd(ConvArgs a, const T* __restrict__ x, const T* __restrict__ w, const T
     for (int k = 0; k < K; ++k) fma_row<V>(p, wf[k], win[u + k]);
     if (SILU) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) p[c] *= sigmoid(p[c]);
+      for (int c = 0; c < V; ++c) {
+        float sg, rest;
+        sigmoid<T>(p[c], sg, rest);
+        p[c] *= sg;
+      }
     }
     Vec<T, V>::store(to, p);
   };
@@ -264,8 +277,9 @@ k_conv_bwd(ConvBwdArgs a, const T* __restrict__ x, const T* __restrict__ w,
         for (int k = 0; k < K; ++k) fma_row<V>(p, wf[k], win[k]);
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-          const float sg = sigmoid(p[c]);
-          dp[c] *= fmaf(p[c] * sg, 1.f - sg, sg);
+          float sg, rest;
+          sigmoid<T>(p[c], sg, rest);
+          dp[c] *= fmaf(p[c] * sg, rest, sg);
         }
       }
       if (mine) {
