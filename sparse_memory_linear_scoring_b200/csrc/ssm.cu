@@ -288,7 +288,8 @@ k_ssm_step(SsmArgs a, const Tin* __restrict__ x, const float* __restrict__ dt,
   const float Ah = A[h], Dh = D ? D[h] : 0.f;
   for (int t = 0; t < a.T; ++t) {
     const float d = dt[row_off(a.sdt, b, h, t)];
-    const float da = expf(d * Ah);
+    const float g = d * Ah, e = expf(g);
+    const float da = e == 0.f ? 0.f : fmaf(e, fmaf(d, Ah, -g), e);  // exp of the unrounded product
     const Tin* bp = Bm + row_off(a.sB, b, gr, t) + lane * 4;
     const Tin* cp = Cm + row_off(a.sC, b, gr, t) + lane * 4;
     float bv[4], cv[4], xv[kStepRows];

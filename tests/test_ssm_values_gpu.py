@@ -81,3 +81,16 @@ def test_gradients_stay_apart(B, H, G, T, P, N, dtype, layout, name, at, value):
         z = torch.zeros((), device="cuda")
         R.close(torch.where(fin, out[n], z.to(out[n].dtype)), torch.where(fin, ref[n], z.double()),
                 (k16 if n in ("x", "Bm", "Cm") else k32) * mag[n], "d" + n)
+
+
+def test_step_decay_is_exact():
+    """exp(dt A) of one step for decays down to e^-80: expf's 2 units in the last place and
+    two roundings, 2^-21 of the state, however large |dt A| is."""
+    H = 512
+    dt = torch.linspace(0.01, 9.99, H, device="cuda").view(1, H, 1)
+    A = -torch.full((H,), 8.0, device="cuda") + torch.linspace(0, 0.1, H, device="cuda")
+    S = torch.linspace(1, 2, 256, device="cuda").view(1, 1, 16, 16).repeat(1, H, 1, 1)
+    z = torch.zeros(1, H, 1, 16, device="cuda")
+    want = S.double() * torch.exp(dt.double() * A.double()[None, :, None])[..., None]
+    sdm.ssm_step(z, dt, A, z, z, S)
+    assert float(((S.double() - want) / want).abs().max()) <= 2.0 ** -21
