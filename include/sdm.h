@@ -359,7 +359,10 @@ SDM_API int sdm_conv_forward(const void* x, const void* w, const void* bias, voi
  * Gradients: dx (x's type), dw [H][d][K], dbias [H][d] (NULL: not wanted) and
  * dstate0 [B][H][K-1][d] (NULL: not wanted), float32.  state0: the state the
  * forward started from (a copy; NULL for zeros).  dstate: the gradient of the
- * state it left, float32, NULL for 0.  T >= 1, full length: mask dy for padded steps.
+ * state it left, float32, NULL for 0.  T >= 1, full length.  For a padded batch
+ * (finite x): dy = 0 on the padded steps; the state left is then inputs
+ * lengths[b] - K + 1 .. lengths[b] - 1, not the last ones, so its gradient is added
+ * to those rows of dx (of dstate0 before step 0) by the caller, and dstate is NULL.
  */
 SDM_API size_t sdm_conv_backward_workspace_bytes(const sdm_conv_dims* dims);
 SDM_API int sdm_conv_backward(const void* x, const void* w, const void* bias, const void* state0,
@@ -398,13 +401,16 @@ SDM_API int sdm_ssm_forward(const void* x, const float* dt, const float* A, cons
                             const sdm_ssm_views* views, void* workspace, size_t ws_bytes,
                             void* stream);
 
-/* The same for one token or a few (the steps run in order): one kernel, no workspace. */
+/* The same for one token or a few (the steps run in order): one kernel, no workspace.
+ * A row of the batch without a token takes dt = 0. */
 SDM_API int sdm_ssm_step(const void* x, const float* dt, const float* A, const void* Bm,
                          const void* Cm, const float* D, float* S_inout, void* y,
                          const sdm_ssm_dims* dims, const sdm_ssm_views* views, void* stream);
 
 /*
- * Gradients of sdm_ssm_forward at full length.  S0: the state it started from
+ * Gradients of sdm_ssm_forward at full length.  For a padded batch (finite x, Bm,
+ * Cm): dt = 0 and dy = 0 on the padded steps, which leaves S and its gradient as
+ * they are; ddt of those steps is of no use.  S0: the state it started from
  * (NULL: zeros).  dS_T: gradient of the state it left (NULL: 0).  views.y: strides
  * of dy; grad_views.x, dt, B, C: strides of dx, ddt, dB, dC (grad_views.y is not
  * used).  dx, dB, dC have the inputs' type; ddt, dA [H], dD [H] (NULL: not
@@ -451,6 +457,11 @@ SDM_API int sdm_block_pool(const void* k, void* kc, int32_t first, const sdm_blo
  * best first, lower index at ties, then -1.  Blocks that score -inf or NaN are not
  * listed; a query with p < 0 gets -1 throughout.  Scores are float64 sums.  n_means
  * >= (Tk - 1) / block means have to be there.
+ * lengths is for caches: the queries are the last Tq keys of each row.  A batch of
+ * prompts padded behind, as sdm_conv_forward and sdm_ssm_forward take it, has its
+ * queries at positions 0 .. T - 1 (Tq = Tk = T) and needs no lengths, here or below:
+ * a live query only sees keys and lists blocks at or before it.  Padded keys and
+ * values should be finite, padded rows of o are to be ignored, those of d_o 0.
  */
 SDM_API int sdm_block_select(const void* q, const void* kc, int32_t n_means,
                              const int32_t* lengths, int32_t* idx, const sdm_block_dims* dims,

@@ -64,7 +64,9 @@ def conv_backward(x, w, dy, bias=None, state0=None, dstate=None, *, silu: bool =
                   workspace: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
     """Gradients of conv_forward at full length (sdm_conv_backward).  state0: the state
     the forward started from (a copy; None for zeros); dstate [B,H,K-1,d] float32: the
-    gradient of the state it left.  Returns x (x's dtype), w [H,d,K] and, where bias /
+    gradient of the state it left.  For a padded batch: dy = 0 behind each row's length, and
+    the gradient of the state left, which are the K - 1 inputs before that, is added to
+    their rows of the result instead of given as dstate.  Returns x (x's dtype), w [H,d,K] and, where bias /
     state0 or dstate are given, bias [H,d] and state [B,H,K-1,d], float32."""
     if stream is not None:
         return _on(stream, x, _host().conv_backward, x, w, dy, bias, state0, dstate, bool(silu), workspace)
@@ -95,7 +97,7 @@ def ssm_forward(x, dt, A, Bm, Cm, S, D=None, *, lengths: Optional[torch.Tensor] 
 def ssm_step(x, dt, A, Bm, Cm, S, D=None, *, y: Optional[torch.Tensor] = None,
              stream=None) -> torch.Tensor:
     """ssm_forward for one token or a few at a time (sdm_ssm_step): one kernel that
-    reads and writes S once, no workspace."""
+    reads and writes S once, no workspace.  A row without a token takes dt = 0."""
     if stream is not None:
         return _on(stream, x, _host().ssm_forward, True, x, dt, A, Bm, Cm, S, D, None, y, None)
     return _host().ssm_forward(True, x, dt, A, Bm, Cm, S, D, None, y, None)
@@ -103,7 +105,8 @@ def ssm_step(x, dt, A, Bm, Cm, S, D=None, *, y: Optional[torch.Tensor] = None,
 
 def ssm_backward(x, dt, A, Bm, Cm, S0, dy, dS_T=None, *, D=None,
                  workspace: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
-    """Gradients of ssm_forward at full length (sdm_ssm_backward).  S0: the state it
+    """Gradients of ssm_forward at full length (sdm_ssm_backward); for a padded batch, dt = 0
+    and dy = 0 behind each row's length.  S0: the state it
     started from (a copy; None for zeros); dS_T: the gradient of the state it left
     (None: 0).  Returns x, Bm, Cm (x's dtype), dt [B,H,T], A [H], S0 [B,H,d_v,d_k] and,
     where D is given, D [H], float32."""
@@ -128,7 +131,8 @@ def block_select(q, kc, *, n_sel: int, block: int = 64, Tk: Optional[int] = None
     """Lists of blocks per query and key head (sdm_block_select): the query's own block,
     then the best n_sel - 1 before it by the group's summed q . kc, best first, lower
     index at ties, then -1.  q [B,H,Tq,d] are the last Tq of Tk keys (default Tk = Tq),
-    or of lengths[b] <= Tk in row b; kc [B,G,n,d] from block_pool.  Returns idx
+    or of lengths[b] <= Tk in row b (caches; a batch of prompts padded behind needs no
+    lengths, here or in block_forward: its live queries see nothing behind them); kc [B,G,n,d] from block_pool.  Returns idx
     [B,G,Tq,n_sel] int32."""
     if stream is not None:
         return _on(stream, q, _host().block_select, q, kc, n_sel, block, Tk, lengths)
