@@ -89,3 +89,19 @@ def test_keys_with_a_common_part(H, G, Tq, Tk, d, block, layout):
     o, lse = sdm.block_forward(q, k, v, idx, block=block, return_lse=True)
     out = sdm.block_backward(q, k, v, idx, o, lse, do, block=block)
     assert _norm(out["q"], ref["q"]) <= 0.004
+
+
+@pytest.mark.parametrize("H,G,Tq,Tk,d,block", [
+    (8, 2, 1, 600, 64, 64), (8, 8, 20, 600, 64, 64), (8, 2, 600, 600, 64, 64), (12, 2, 900, 900, 128, 64),
+    (6, 3, 500, 500, 32, 128)])
+def test_norms(H, G, Tq, Tk, d, block):
+    """bf16 results and gradients: 0.00165 of the norm is the rounding of a result with
+    evenly spread mantissas; one more rounding of an operand adds its square at most once."""
+    q, k, v, g = _make(2, H, G, Tq, Tk, d, BF, "token")
+    idx = R.select(q, R.pool(k, block), 6, block, Tk)
+    do = torch.randn(q.shape, generator=g, device="cuda").to(BF)
+    ref = R.block_attention(q, k, v, idx, block, d ** -0.5, None, do)
+    o, lse = sdm.block_forward(q, k, v, idx, block=block, return_lse=True)
+    out = sdm.block_backward(q, k, v, idx, o, lse, do, block=block)
+    for n, a in (("o", o), *out.items()):
+        assert _norm(a, ref[n]) <= 2 ** 0.5 * 0.00165 * 1.05, n

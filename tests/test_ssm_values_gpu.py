@@ -94,3 +94,22 @@ def test_step_decay_is_exact():
     want = S.double() * torch.exp(dt.double() * A.double()[None, :, None])[..., None]
     sdm.ssm_step(z, dt, A, z, z, S)
     assert float(((S.double() - want) / want).abs().max()) <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("B,H,G,T,P,N", [(2, 8, 2, 64, 64, 64), (2, 8, 2, 500, 64, 64), (2, 4, 4, 500, 128, 128),
+                                         (2, 4, 1, 500, 64, 128), (24, 12, 1, 200, 128, 64)])
+def test_norms(B, H, G, T, P, N):
+    """bf16 results and gradients: 0.00165 of the norm is the rounding of a result with
+    evenly spread mantissas; y and dx have one more rounding of an operand in each term,
+    which adds its square at most once.  One part of the weights in dB and dC would make
+    0.0027 in a short call."""
+    a, g = _make(B, H, G, T, P, N, BF)
+    dy = torch.randn(B, T, H, P, generator=g, device="cuda").to(BF).transpose(1, 2)
+    dS = torch.randn(B, H, P, N, generator=g, device="cuda") * 0.1
+    S = a["S"].clone()
+    y = sdm.ssm_forward(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], S, a["D"])
+    out = _grads(a, dy, dS)
+    ry, _, _ = R.ssm(**a)
+    ref = R.ssm_grads(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], a["S"], dy, dS, a["D"])
+    for n, got, want in [("y", y, ry)] + [(n, out[n], ref[n]) for n in ("x", "Bm", "Cm")]:
+        assert float((got.double() - want).norm() / want.norm()) <= 2 ** 0.5 * 0.00165 * 1.05, n
