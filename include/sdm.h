@@ -419,7 +419,8 @@ SDM_API int sdm_ssm_step(const void* x, const float* dt, const float* A, const v
  * dy leaves what does not depend on it as it is, as in the forward pass (between a
  * NaN of dy and a later one of x or Bm in the same 64 steps ddt may be NaN).
  * The workspace holds the states and
- * their gradients at chunk starts and grows with T.
+ * their gradients at chunk starts and grows with T; it is sized for views of any
+ * alignment (chunks of 32 steps), of which aligned bf16 views use half.
  */
 SDM_API size_t sdm_ssm_backward_workspace_bytes(const sdm_ssm_dims* dims);
 SDM_API int sdm_ssm_backward(const void* x, const float* dt, const float* A, const void* Bm,
@@ -446,7 +447,7 @@ typedef struct sdm_block_dims {
 typedef struct sdm_block_views { sdm_strides q, k, v, o, kc; } sdm_block_views;
 
 /* Means of the complete blocks first .. Tk / block - 1 of k, into kc: summed in
- * float64, rounded once to k's type. */
+ * float64, rounded to float32 and then to k's type. */
 SDM_API int sdm_block_pool(const void* k, void* kc, int32_t first, const sdm_block_dims* dims,
                            const sdm_block_views* views, void* stream);
 

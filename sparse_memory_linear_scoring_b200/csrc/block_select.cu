@@ -14,8 +14,10 @@ namespace sdm {
 
 // ---------------------------------------------------------------- means
 // A CTA per block: a thread sums a share of the rows of one 4-column piece.  The sums
-// are double: exact for bf16 keys whatever the order, so the means (and with
-// them the lists) do not depend on how the rows are shared out.
+// are double: exact for bf16 keys whose exponents in a column lie within 2^38 of one another
+// (8 bits each, 7 more for 128 rows), so there the means (and with them the lists) do not
+// depend on how the rows are shared out.  The mean is rounded to float32 and then to the
+// keys' type.
 template <typename Tin>
 __global__ void __launch_bounds__(128)
 k_blk_pool(BlkArgs a, sdm_strides skc, const Tin* __restrict__ k, Tin* __restrict__ kc, int first,

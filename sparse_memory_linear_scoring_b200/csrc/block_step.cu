@@ -8,6 +8,7 @@
 // way (cp.async) while one is computed, with a running maximum and sum; the warps of up
 // to 8 CTAs of a cluster share a query and join through distributed shared memory, so
 // one launch without a workspace fills the card from few sequences.
+// P is rounded to bf16 for its product as in block_tc.cu.
 // block_attn.cu has the formulas, and the CUDA-core kernel for views that cannot be read
 // in 16-byte pieces; per head and key that one needs about 100 instructions where a tile
 // needs 200 a piece in all (64 sequences of up to 4096 keys, 16 heads of 64 on 4: 35 us

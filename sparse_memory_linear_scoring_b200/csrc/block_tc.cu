@@ -8,6 +8,8 @@
 //   softmax of the thread's own row from TMEM, P as bf16 over the queries' place,
 //   O = P V (tcgen05.mma; V is MN-major as it lies, so nothing is transposed),
 //   O over the row's largest element as halves, through shared memory to the parts.
+// P is rounded to bf16 for its product, the sum that divides it is of the unrounded weights in
+// float32: o is 0.0021 of its norm off, where the result's rounding alone makes 0.0017.
 // The products take a few percent of the time.  What bounds a tile is the softmax, the
 // conversion of O, the gather and the way out, 47 warp instructions a row (warp-level
 // fragments, where four lanes share each row's maxima and sums and every operand goes

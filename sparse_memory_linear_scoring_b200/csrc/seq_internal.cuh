@@ -12,7 +12,6 @@
 namespace sdm {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr size_t kSeqMaxSmem = 227 * 1024;
 
 // Offset of row (b, h, t) of a strided view (elements, 64 bits throughout).
 __host__ __device__ __forceinline__ long long row_off(const sdm_strides& s, int b, int h, int t) {

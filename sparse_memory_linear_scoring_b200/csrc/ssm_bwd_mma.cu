@@ -5,12 +5,14 @@
 // and to their gradients, and, after the carries, the gradients.  What ends in float32
 // (states, ddt, dA, dD, dS0) keeps float32 accuracy: products of bf16 inputs are exact,
 // and a float32 operand beside a bf16 one is split into three bf16 parts (rest below
-// 2^-24).  W G, whose product ends in dx, is rounded once; W dt R is two parts: in
+// 2^-24).  W G, whose product ends in dx, is rounded once, and dx takes the first of dSin's
+// parts alone: one rounding in each term (dx is 0.0020 of its norm off, where the result's
+// rounding alone makes 0.0017).  W dt R is two parts: in
 // a short call it makes most of dB and dC, and one part's error (0.0021 of their norm) would
 // add to the results' own (0.0017).  Per chunk and head 14 products of 64 x 64 x 64 at
 // widths of 64, eight of them for the splits; the tiles of x, dy, B, C and the two float32
-// states that a CTA reads (72 KB) bound it.  4 x 2048 steps, 8 heads of 64 x 64: 17 us the
-// contributions, 51 the gradients (CUDA cores: 98 and 258).
+// states that a CTA reads (72 KB) bound it.  4 x 2048 steps, 8 heads of 64 x 64: 18 us the
+// contributions, 52 the gradients (CUDA cores: 98 and 258).
 #include <type_traits>
 
 #include "mma_dev.cuh"
